@@ -23,6 +23,9 @@ __all__ = [
     "q4_dequant_f32_run", "q4_dequant_bf16_run", "vec4_read_probe_run",
     "q4gemv_device_status", "q4gemm_set_wait_timeout_ns", "q4gemv_set_overlapped_launch",
     "q4gemv_bounds_violations", "q4gemv_grouped_split",
+    "q4moe_route_run", "q4moe_route_workspace", "q4moe_gemm_run", "q4moe_gemm_workspace",
+    "q4_block_norm_run", "q4moe_block_run", "q4moe_block_workspace",
+    "Q4_F32", "Q4_BF16", "Q4_ROUTE_SOFTMAX", "Q4_ROUTE_SIGMOID",
     "Q4_OK", "Q4_ERR_INVALID_ARG", "Q4_ERR_UNSUPPORTED", "Q4_ERR_MISALIGNED",
     "Q4_ERR_CUDA", "Q4_ERR_TIMEOUT", "Q4_EPILOGUE_NONE", "Q4_EPILOGUE_SWIGLU",
     "Q4_RUN_OVERLAPPED", "Q4_RUN_EXACT_X", "Q4_RUN_WAIT_TIMEOUT",
@@ -35,6 +38,8 @@ HEADER = os.path.join(_ROOT, "include", "q4gemv.h")
 Q4_OK, Q4_ERR_INVALID_ARG, Q4_ERR_UNSUPPORTED, Q4_ERR_MISALIGNED, Q4_ERR_CUDA, Q4_ERR_TIMEOUT = range(6)
 Q4_EPILOGUE_NONE, Q4_EPILOGUE_SWIGLU = 0, 1
 Q4_RUN_OVERLAPPED, Q4_RUN_EXACT_X, Q4_RUN_WAIT_TIMEOUT = 0x1, 0x2, 0x4
+Q4_F32, Q4_BF16 = 0, 1
+Q4_ROUTE_SOFTMAX, Q4_ROUTE_SIGMOID = 0, 1
 
 
 def library_path() -> str:
@@ -66,6 +71,27 @@ class _RunOptions(ctypes.Structure):
 class _Segment(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales_f16", ctypes.c_void_p), ("zeros_u4_or_null", ctypes.c_void_p),
                 ("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("N", ctypes.c_int64)]
+
+
+class _BlockNorm(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("top_k", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("R", ctypes.c_int64), ("y", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("x", ctypes.c_void_p), ("post_gamma", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("gate_stride", ctypes.c_int64), ("pre_gamma", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("out_norm", ctypes.c_void_p), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class _MoeBlock(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "E", "top_k", "H", "inner", "group", "dtype", "score",
+                                               "renormalize")] +
+                [(n, ctypes.c_float) for n in ("route_scale", "residual_scale", "eps")] +
+                [(n, ctypes.c_void_p) for n in ("up_codes", "up_scales_f16", "up_zeros_u4_or_null", "down_codes",
+                                                "down_scales_f16", "down_zeros_u4_or_null", "logits", "bias_or_null",
+                                                "token_mask_or_null", "a", "x", "post_gamma", "gate")] +
+                [("gate_stride", ctypes.c_int64)] +
+                [(n, ctypes.c_void_p) for n in ("pre_gamma", "ids", "route_weights", "out", "out_norm",
+                                                "workspace")] +
+                [("workspace_bytes", ctypes.c_int64)])
 
 
 _lock = threading.Lock()
@@ -111,7 +137,19 @@ def lib() -> ctypes.CDLL:
             L.q4gemv_bounds_violations.argtypes = [_vp]
             L.q4gemv_grouped_split.argtypes = [ctypes.POINTER(_i64), _i32, _i64, _i32, _i32,
                                                ctypes.POINTER(_i32), ctypes.POINTER(_i32)]
-            for f in ("q4gemv_pack_info", "q4gemv_run", "q4gemv_fused_run", "q4gemv_grouped_run", "q4_0_gemv_run",
+            L.q4moe_route_workspace.argtypes = [_i32, _i32, _i32]
+            L.q4moe_gemm_workspace.argtypes = [_i64, _i64, _i64, _i64, _i32, _i32]
+            L.q4moe_block_workspace.argtypes = [_i32] * 6
+            for f in ("q4moe_route_workspace", "q4moe_gemm_workspace", "q4moe_block_workspace"):
+                getattr(L, f).restype = _i64
+            L.q4moe_route_run.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _vp,
+                                          _vp, _vp, _vp, _i64, _opt, _vp]
+            L.q4moe_gemm_run.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i32, _i32,
+                                         _i32, _vp, _i64, _opt, _vp]
+            L.q4_block_norm_run.argtypes = [ctypes.POINTER(_BlockNorm), _opt, _vp]
+            L.q4moe_block_run.argtypes = [ctypes.POINTER(_MoeBlock), _opt, _vp]
+            for f in ("q4moe_route_run", "q4moe_gemm_run", "q4_block_norm_run", "q4moe_block_run",
+                      "q4gemv_pack_info", "q4gemv_run", "q4gemv_fused_run", "q4gemv_grouped_run", "q4_0_gemv_run",
                       "q8_0_gemv_run",
                       "q4gemm_run", "f32gemv_run", "q4gemv_run_ex", "q4gemv_fused_run_ex", "q4gemv_grouped_run_ex",
                       "q4gemm_run_ex",
@@ -393,3 +431,175 @@ def vec4_read_probe_run(buf, nbytes, partial, blocks=0, stream=None, check=True)
     if check:
         _check(st, "vec4_read_probe_run")
     return used.value
+
+
+# ------------------------------------------------------------ mixture of experts
+
+def _dtype(t):
+    """Q4_F32 or Q4_BF16 of a tensor or a torch dtype (an integer passes through)."""
+    if isinstance(t, int):
+        return t
+    import torch
+    d = getattr(t, "dtype", t)
+    if d == torch.float32:
+        return Q4_F32
+    if d == torch.bfloat16:
+        return Q4_BF16
+    raise ValueError(f"float32 or bfloat16 expected, got {d}")
+
+
+def _same(t, name, dtype):
+    """Address of an activation array of the call's type (None passes through)."""
+    if t is not None and _dtype(t) != dtype:
+        raise ValueError(f"{name}: has another type than the call's other activations ({t.dtype})")
+    return _addr(t, name)
+
+
+def _ints(t, name):
+    """Address of an int32 array (None passes through)."""
+    if t is not None and not isinstance(t, int):
+        import torch
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name}: int32 expected, got {t.dtype}")
+    return _addr(t, name, 4)
+
+
+def _floats(t, name):
+    """Address of a binary32 array (None passes through)."""
+    if t is not None and not isinstance(t, int):
+        import torch
+        if t.dtype != torch.float32:
+            raise ValueError(f"{name}: float32 expected, got {t.dtype}")
+    return _addr(t, name, 4)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _workspace(n, where):
+    if n < 0:
+        raise Q4Error(Q4_ERR_UNSUPPORTED, where)
+    return n
+
+
+def q4moe_route_workspace(T, E, top_k) -> int:
+    """Bytes of workspace q4moe_route_run needs."""
+    return _workspace(lib().q4moe_route_workspace(int(T), int(E), int(top_k)), "q4moe_route_workspace")
+
+
+def q4moe_gemm_workspace(R, Tx, N, K, E, dtype) -> int:
+    """Bytes of workspace q4moe_gemm_run needs (dtype: that of x)."""
+    return _workspace(lib().q4moe_gemm_workspace(int(R), int(Tx), int(N), int(K), int(E), _dtype(dtype)),
+                      "q4moe_gemm_workspace")
+
+
+def q4moe_block_workspace(T, E, top_k, H, inner, dtype) -> int:
+    """Bytes of workspace q4moe_block_run needs."""
+    return _workspace(lib().q4moe_block_workspace(int(T), int(E), int(top_k), int(H), int(inner), _dtype(dtype)),
+                      "q4moe_block_workspace")
+
+
+def q4moe_route_run(logits, ids, weights, offsets, rows, pos, workspace, bias=None, token_mask=None,
+                    score=Q4_ROUTE_SOFTMAX, renormalize=True, scale=1.0, flags=None, stream=None, check=True) -> int:
+    """The top_k experts of each token (ids [T, top_k], weights), and the rows grouped by
+    expert (offsets [E + 1], rows [T * top_k], pos [T, top_k])."""
+    T, E = logits.shape
+    k = ids.shape[1]
+    _need(ids.shape[0] == T and tuple(weights.shape) == (T, k) and tuple(pos.shape) == (T, k) and
+          rows.numel() == T * k and offsets.numel() == E + 1 and (bias is None or bias.numel() == E) and
+          (token_mask is None or token_mask.numel() == T), "q4moe_route_run: shapes do not agree")
+    st = lib().q4moe_route_run(_floats(logits, "logits"), _floats(bias, "bias"), _addr(token_mask, "token_mask", 1),
+                               T, E, k, int(score), 1 if renormalize else 0, float(scale), _ints(ids, "ids"),
+                               _floats(weights, "weights"), _ints(offsets, "offsets"), _ints(rows, "rows"),
+                               _ints(pos, "pos"), _addr(workspace, "workspace", 1), workspace.numel(),
+                               _options(flags, None), _stream(stream))
+    if check:
+        _check(st, "q4moe_route_run")
+    return st
+
+
+def q4moe_gemm_run(codes, scales_f16, zeros_u4_or_null, x, rows, offsets, y, workspace, group=32,
+                   epilogue=Q4_EPILOGUE_NONE, flags=None, wait_timeout_ns=None, stream=None, check=True) -> int:
+    """y[r] = W_e x[rows[r]] over stacked experts codes [E, N, K/2] (rows None: x[r])."""
+    E, N, half = codes.shape
+    Tx, K = x.shape
+    R = y.shape[0]
+    d = _dtype(x)
+    _need(K == 2 * half and y.shape[1] == (N // 2 if epilogue == Q4_EPILOGUE_SWIGLU else N) and
+          tuple(scales_f16.shape) == (E, N, K // group) and offsets.numel() == E + 1 and
+          (zeros_u4_or_null is None or tuple(zeros_u4_or_null.shape) == (E, N, (K // group + 1) // 2)) and
+          (rows is None or rows.numel() == R), "q4moe_gemm_run: shapes do not agree")
+    st = lib().q4moe_gemm_run(_addr(codes, "codes", 1), _addr(scales_f16, "scales_f16", 2),
+                              _addr(zeros_u4_or_null, "zeros_u4_or_null", 1), _addr(x, "x"), _ints(rows, "rows"),
+                              _ints(offsets, "offsets"), _same(y, "y", d), E, R, Tx, N, K, int(group), d,
+                              int(epilogue), _addr(workspace, "workspace", 1), workspace.numel(),
+                              _options(flags, wait_timeout_ns), _stream(stream))
+    if check:
+        _check(st, "q4moe_gemm_run")
+    return st
+
+
+def _gate_stride(gate, T, H):
+    if gate is None or gate.dim() == 1:
+        _need(gate is None or gate.numel() == H, "gate: [H] or [T, H] expected")
+        return 0
+    _need(tuple(gate.shape) == (T, H), "gate: [H] or [T, H] expected")
+    return H
+
+
+def q4_block_norm_run(y, x, out, pos=None, weights=None, post_gamma=None, gate=None, residual_scale=1.0,
+                      pre_gamma=None, out_norm=None, eps=1e-6, flags=None, stream=None, check=True) -> int:
+    """out = residual_scale x + gate norm(b), out_norm = norm(out): b is the weighted sum of
+    the rows pos of y, or y itself (pos None)."""
+    T, H = x.shape
+    k = pos.shape[1] if pos is not None else 0
+    d = _dtype(x)
+    _need(y.shape[1] == H and tuple(out.shape) == (T, H) and (out_norm is None or tuple(out_norm.shape) == (T, H)) and
+          (pos is None or (pos.shape[0] == T and weights is not None and tuple(weights.shape) == (T, k))) and
+          (post_gamma is None or post_gamma.numel() == H) and (pre_gamma is None or pre_gamma.numel() == H),
+          "q4_block_norm_run: shapes do not agree")
+    a = _BlockNorm(T, H, k, d, y.shape[0], _same(y, "y", d), _ints(pos, "pos"), _floats(weights, "weights"),
+                   _addr(x, "x"), _floats(post_gamma, "post_gamma"), _same(gate, "gate", d),
+                   _gate_stride(gate, T, H), _floats(pre_gamma, "pre_gamma"), _same(out, "out", d),
+                   _same(out_norm, "out_norm", d), float(residual_scale), float(eps))
+    st = lib().q4_block_norm_run(ctypes.byref(a), _options(flags, None), _stream(stream))
+    if check:
+        _check(st, "q4_block_norm_run")
+    return st
+
+
+def q4moe_block_run(up, down, logits, a, x, out, out_norm, ids, route_weights, workspace, group=32,
+                    score=Q4_ROUTE_SOFTMAX, renormalize=True, route_scale=1.0, bias=None, token_mask=None,
+                    post_gamma=None, gate=None, residual_scale=1.0, pre_gamma=None, eps=1e-6, flags=None,
+                    wait_timeout_ns=None, stream=None, check=True) -> int:
+    """A mixture-of-experts block in one call: route, gate and up, down, norms and residual.
+    up: (codes [E, 2 inner, H/2], scales, zeros or None); down: (codes [E, H, inner/2], ...)."""
+    T, E = logits.shape
+    H = x.shape[1]
+    inner = 2 * down[0].shape[2]
+    k = ids.shape[1]
+    d = _dtype(x)
+    for (codes, scales, zeros), N, K in ((up, 2 * inner, H), (down, H, inner)):
+        _need(tuple(codes.shape) == (E, N, K // 2) and tuple(scales.shape) == (E, N, K // group) and
+              (zeros is None or tuple(zeros.shape) == (E, N, (K // group + 1) // 2)),
+              "q4moe_block_run: shapes of the weights do not agree")
+    _need(x.shape[0] == T and tuple(a.shape) == (T, H) and tuple(out.shape) == (T, H) and
+          (out_norm is None or tuple(out_norm.shape) == (T, H)) and tuple(ids.shape) == (T, k) and
+          tuple(route_weights.shape) == (T, k) and (bias is None or bias.numel() == E) and
+          (token_mask is None or token_mask.numel() == T) and (post_gamma is None or post_gamma.numel() == H) and
+          (pre_gamma is None or pre_gamma.numel() == H), "q4moe_block_run: shapes do not agree")
+    g = _MoeBlock(T, E, k, H, inner, int(group), d, int(score), 1 if renormalize else 0, float(route_scale),
+                  float(residual_scale), float(eps), _addr(up[0], "up codes", 1), _addr(up[1], "up scales", 2),
+                  _addr(up[2], "up zeros", 1), _addr(down[0], "down codes", 1), _addr(down[1], "down scales", 2),
+                  _addr(down[2], "down zeros", 1), _floats(logits, "logits"), _floats(bias, "bias"),
+                  _addr(token_mask, "token_mask", 1), _same(a, "a", d), _addr(x, "x"),
+                  _floats(post_gamma, "post_gamma"), _same(gate, "gate", d), _gate_stride(gate, T, H),
+                  _floats(pre_gamma, "pre_gamma"), _ints(ids, "ids"), _floats(route_weights, "route_weights"),
+                  _same(out, "out", d), _same(out_norm, "out_norm", d), _addr(workspace, "workspace", 1),
+                  workspace.numel())
+    st = lib().q4moe_block_run(ctypes.byref(g), _options(flags, wait_timeout_ns), _stream(stream))
+    if check:
+        _check(st, "q4moe_block_run")
+    return st

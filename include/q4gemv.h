@@ -325,6 +325,141 @@ Q4_API int q4gemm_set_wait_timeout_ns(uint64_t ns);
  * Returns the previous setting (0 or 1). */
 Q4_API int q4gemv_set_overlapped_launch(int enable);
 
+/* ---- mixture of experts over int4 weights ------------------------------------------
+ * The feed-forward path of a mixture of experts whose E weight matrices are stacked in the
+ * MatMulNBits layout: codes [E][N][K/2], scales [E][N][K/g], zeros [E][N][ceil(K/g/2)].
+ * Groups, rows and counts stay on the device: no call reads them on the host, so a step of
+ * these calls can be captured in a CUDA graph and replayed for other tokens.  The pages
+ * describe single matrices and have no counterpart.
+ *
+ * Activations are binary32 (Q4_F32) or bfloat16 (Q4_BF16), outputs have the type of the
+ * inputs; router logits, routing weights and norm weights are binary32.  Workspaces are
+ * device memory of the caller, 256-byte aligned; their contents mean nothing between calls
+ * and one workspace may not serve two calls that may run at the same time.  Too small a
+ * workspace is Q4_ERR_INVALID_ARG.  opts (NULL: the defaults) takes Q4_RUN_OVERLAPPED and
+ * Q4_RUN_WAIT_TIMEOUT; any other flag or a nonzero reserved field is Q4_ERR_INVALID_ARG.
+ * Overlapped, a call's first kernel may be scheduled while the kernel before it in the
+ * stream still runs, and waits for it before it reads or writes any array. */
+#define Q4_F32 0
+#define Q4_BF16 1
+#define Q4_ROUTE_SOFTMAX 0
+#define Q4_ROUTE_SIGMOID 1
+
+/* Bytes of workspace q4moe_route_run needs (-1 for sizes it does not serve). */
+Q4_API int64_t q4moe_route_workspace(int32_t T, int32_t E, int32_t top_k);
+
+/* Router: each token's top_k experts, their weights, and the rows grouped by expert.
+ *   sel[t][e] = logits[t][e] + bias[e] (one binary32 addition; bias NULL: the logit)
+ *   The top_k largest sel are chosen in descending order, equal ones by lower expert.
+ *   An expert whose sel is NaN or -inf is never chosen, nor is any by a token whose
+ *   token_mask byte is 0: the places left over hold id -1, weight 0 and pos -1.
+ *   Weights, from the logits without the bias (logits finite, -inf or NaN; NaN counts as
+ *   -inf), S the token's chosen experts:
+ *     Q4_ROUTE_SOFTMAX: exp(l_j) / sum_e exp(l_e), the sum over S if renormalize, else
+ *     over all experts;
+ *     Q4_ROUTE_SIGMOID: s_j = 1 / (1 + exp(-l_j)), divided by (sum_S s + 1e-20) if
+ *     renormalize;
+ *   all times scale.
+ *   logits : device float [T][E];  bias : device float [E] or NULL
+ *   token_mask : device uint8 [T] or NULL
+ *   ids : device int32 [T][top_k];  weights : device float [T][top_k]
+ *   offsets : device int32 [E + 1], rows [offsets[e], offsets[e+1]) belong to expert e
+ *   rows : device int32 [T * top_k], the token of each row; within an expert tokens
+ *     ascend; -1 from offsets[E] on
+ *   pos : device int32 [T][top_k], the row of each choice, or -1
+ * 1 <= E <= 1024, 1 <= top_k <= min(E, 32), T * top_k < 2^31 (Q4_ERR_UNSUPPORTED above
+ * the upper limits).  T == 0 is an empty problem. */
+Q4_API int q4moe_route_run(const float *logits, const float *bias_or_null, const uint8_t *token_mask_or_null, int32_t T,
+                    int32_t E, int32_t top_k, int32_t score, int32_t renormalize, float scale, int32_t *ids,
+                    float *weights, int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace,
+                    int64_t workspace_bytes, const q4_run_options_t *opts, void *stream);
+
+/* Bytes of workspace q4moe_gemm_run needs for R rows of y, x of Tx rows, E experts of
+ * N x K and dtype (-1 for sizes it does not serve). */
+Q4_API int64_t q4moe_gemm_workspace(int64_t R, int64_t Tx, int64_t N, int64_t K, int32_t E, int32_t dtype);
+
+/* Matrix product grouped by expert, ragged sizes:
+ *   y[r] = W_e x[rows[r]]   for r in [offsets[e], offsets[e+1])   (rows NULL: x[r])
+ * epilogue Q4_EPILOGUE_SWIGLU as in q4gemv_fused_run: weight rows 2i / 2i+1 are gate / up,
+ * y[r][i] = silu(g) u, N even.
+ *   x : device [Tx][K], 16-byte aligned (rows NULL: Tx >= R);  y : device [R][N] or
+ *   [R][N/2];  offsets : device int32 [E + 1];  rows : device int32 [R] or NULL
+ * Rows of y that no expert owns are left as they were.  Each offset is clamped to [0, R]
+ * and to no less than the one before it, and a row index outside [0, Tx) reads as a row of
+ * zeros, so no content of the two arrays makes the kernels leave their buffers.
+ * Accuracy: binary32 sums; for Q4_F32 weights and activations are each carried as two
+ * binary16 parts (22 bits and more), for Q4_BF16 the activations are exact and each weight
+ * is rounded once to binary16.  |(q - z) s| < 65504 and finite x, as in the tensor-core
+ * GEMV; each row of x is scaled by its own power of two, so its range is not limited.
+ * 1 <= E <= 1024, R and Tx < 2^31, E * N < 2^31 (Q4_ERR_UNSUPPORTED above). */
+Q4_API int q4moe_gemm_run(const void *codes, const void *scales_f16, const void *zeros_u4_or_null, const void *x,
+                   const int32_t *rows_or_null, const int32_t *offsets, void *y, int32_t E, int64_t R, int64_t Tx,
+                   int64_t N, int64_t K, int32_t group, int32_t dtype, int32_t epilogue, void *workspace,
+                   int64_t workspace_bytes, const q4_run_options_t *opts, void *stream);
+
+/* What follows a block's output (zero-initialise, then fill in). */
+typedef struct {
+    int32_t T, H;              /* tokens, features                                        */
+    int32_t top_k;             /* rows of y summed per token; 0: y[t] is the block output */
+    int32_t dtype;             /* Q4_F32 or Q4_BF16: y, x, gate, out, out_norm            */
+    int64_t R;                 /* rows of y (top_k 0: T)                                  */
+    const void *y;             /* device [R][H]                                           */
+    const int32_t *pos;        /* device [T][top_k], rows of y; outside [0, R): skipped   */
+    const float *weights;      /* device [T][top_k]                                       */
+    const void *x;             /* device [T][H], the residual stream                      */
+    const float *post_gamma;   /* device [H] or NULL: no norm after the block             */
+    const void *gate;          /* device [H] or [T][H], or NULL: 1                        */
+    int64_t gate_stride;       /* 0: one gate for all tokens;  H: one per token           */
+    const float *pre_gamma;    /* device [H] or NULL: no norm before the next block       */
+    void *out;                 /* device [T][H]                                           */
+    void *out_norm;            /* device [T][H], with pre_gamma                           */
+    float residual_scale, eps; /* eps >= 0                                                */
+} q4_block_norm_t;
+
+/* Norms before and after a block, fused with its gate, the scaled residual and the
+ * weighted sum of a token's expert rows, in one pass:
+ *   b = sum_j weights[t][j] y[pos[t][j]]      (top_k 0: y[t])
+ *   p = b / sqrt(mean b^2 + eps) * post_gamma (post_gamma NULL: b)
+ *   out[t] = residual_scale x[t] + gate p
+ *   out_norm[t] = out / sqrt(mean out^2 + eps) * pre_gamma, from out before its rounding
+ * All in binary32, rounded once when stored.  A token none of whose rows count has b = 0.
+ * y, x, out, out_norm 16-byte aligned; 1 <= H <= 16384, top_k <= 32 (Q4_ERR_UNSUPPORTED
+ * above).  T == 0 is an empty problem. */
+Q4_API int q4_block_norm_run(const q4_block_norm_t *args, const q4_run_options_t *opts, void *stream);
+
+/* A mixture-of-experts feed-forward block (zero-initialise, then fill in). */
+typedef struct {
+    int32_t T, E, top_k;       /* tokens, experts, experts per token                      */
+    int32_t H, inner;          /* features of the stream and inside an expert             */
+    int32_t group, dtype;
+    int32_t score, renormalize;
+    float route_scale, residual_scale, eps;
+    const void *up_codes, *up_scales_f16, *up_zeros_u4_or_null;       /* [E][2 inner][H]  */
+    const void *down_codes, *down_scales_f16, *down_zeros_u4_or_null; /* [E][H][inner]    */
+    const float *logits;       /* device [T][E]                                           */
+    const float *bias_or_null; /* device [E]                                              */
+    const uint8_t *token_mask_or_null;
+    const void *a;             /* device [T][H], the normed input of the experts          */
+    const void *x;             /* device [T][H], the residual stream                      */
+    const float *post_gamma;
+    const void *gate;
+    int64_t gate_stride;
+    const float *pre_gamma;
+    int32_t *ids;              /* device [T][top_k] out                                   */
+    float *route_weights;      /* device [T][top_k] out                                   */
+    void *out, *out_norm;      /* device [T][H] out                                       */
+    void *workspace;
+    int64_t workspace_bytes;
+} q4moe_block_t;
+
+/* Bytes of workspace q4moe_block_run needs (-1 for sizes it does not serve). */
+Q4_API int64_t q4moe_block_workspace(int32_t T, int32_t E, int32_t top_k, int32_t H, int32_t inner, int32_t dtype);
+
+/* q4moe_route_run, q4moe_gemm_run (gate and up, SwiGLU), q4moe_gemm_run (down) and
+ * q4_block_norm_run in a row, as one call; the kernels after the first are launched
+ * overlapped among themselves. */
+Q4_API int q4moe_block_run(const q4moe_block_t *args, const q4_run_options_t *opts, void *stream);
+
 /* ---- test and measurement exports (not part of the GEMV API proper) ---------------- */
 
 /* Write the dequantised matrix w[N][K] = (q - z) * s as float, with the same in-register
