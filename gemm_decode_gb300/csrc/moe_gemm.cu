@@ -1,122 +1,130 @@
-// moe_gemm.cu -- matrix product grouped by expert over int4 weights, ragged sizes.
-//
-//   y[r] = W_e x[rows[r]],  r in [offsets[e], offsets[e+1]),  w = (q - z) s
-//
-// A CTA computes 64 weight rows by 32 rows of x of one expert: weights are dequantised
-// into shared memory 32 k at a time, sums are binary32.
-#include <cuda_bf16.h>
+// moe_gemm.cu -- host side of the matrix product grouped by expert (moe_gemm_kernel.cuh):
+// workspace, tensor maps, choice of the tile, launches.
+#include <algorithm>
 
-#include "q4_moe.cuh"
+#include "moe_gemm_kernel.cuh"
 
 namespace q4 {
 
-namespace {
-constexpr int TN = 64, TM = 32, TK = 32;
+unsigned int *gemm_status_word();
 
-__device__ __forceinline__ float load_x(const MoeGemmArgs &g, int64_t row, int k) {
-    const int64_t at = row * g.K + k;
-    return g.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(g.x)[at]) : static_cast<const float *>(g.x)[at];
+namespace {
+
+int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// Workspace: prepared x, its scales, arrival counters, partial sums.
+struct Layout {
+    int64_t xscale, arrived, partial, total;
+};
+
+// Tile: rows of x per item.  One weight tile with 32 rows of x streams the weights with the
+// most copies in flight; 256 weight rows by 128 rows of x read each row of x for twice as
+// many products.
+struct Tile {
+    int rt, nt;
+};
+Tile tile_of(int64_t R, int E) { return R > 24 * static_cast<int64_t>(E) ? Tile{2, 128} : Tile{1, 32}; }
+
+Layout layout_of(int64_t R, int64_t Tx, int64_t K, int E, bool bf16) {
+    const Tile t = tile_of(R, E);
+    const int64_t ctas = device_info().sms;
+    Layout l;
+    l.xscale = round256((Tx + 1) * K * (bf16 ? 2 : 4));
+    l.arrived = l.xscale + round256(4 * (Tx + 1));
+    l.partial = l.arrived + round256(4 * ctas);
+    l.total = l.partial + 2 * ctas * 4 * t.rt * 128 * t.nt;
+    return l;
 }
-__device__ __forceinline__ void store_y(const MoeGemmArgs &g, int64_t at, float v) {
-    if (g.bf16) static_cast<__nv_bfloat16 *>(g.y)[at] = __float2bfloat16_rn(v);
-    else static_cast<float *>(g.y)[at] = v;
+
+bool encode_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t inner, int64_t rows,
+               int64_t stride, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+    const cuuint32_t box[2] = {box_inner, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode(map, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+template <int PARTS, int RT, int NT>
+int launch_tile(const CUtensorMap &codes, const CUtensorMap &x, const MoeKernelArgs &g, cudaStream_t stream) {
+    using S = MoeShape<PARTS, RT, NT>;
+    auto kern = moe_gemm_kernel<PARTS, RT, NT>;
+    static std::atomic<bool> configured[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(S::smem(kMaxExperts)));
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            set_cuda_error(e);
+            return Q4_ERR_CUDA;
+        }
+        if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
+    return launch_overlappable(kern, dim3(static_cast<unsigned>(device_info().sms)), dim3(S::kThreads), S::smem(g.E),
+                               stream, true, codes, x, g);
+}
+
 }  // namespace
 
-__global__ void __launch_bounds__(256) moe_gemm_kernel(const MoeGemmArgs g) {
-    __shared__ float ws[TK][TN + 1], xs[TK][TM + 1];
-    __shared__ int tile_e, tile_r0, tile_rows;
-    wait_prior_grid();
-    allow_next_grid();
-    if (threadIdx.x == 0) {
-        int left = blockIdx.y, hi = min(max(g.offsets[0], 0), g.R);
-        tile_e = -1;
-        for (int e = 0; e < g.E; ++e) {
-            const int lo = hi;
-            hi = max(lo, min(g.offsets[e + 1], g.R));   // an offset that falls: an empty expert
-            const int tiles = (hi - lo + TM - 1) / TM;
-            if (left < tiles) {
-                tile_e = e;
-                tile_r0 = lo + left * TM;
-                tile_rows = min(TM, hi - tile_r0);
-                break;
-            }
-            left -= tiles;
-        }
-    }
-    __syncthreads();
-    if (tile_e < 0) return;
-    const int n0 = blockIdx.x * TN;
-    const int nb = g.K / g.group, zrow = (nb + 1) / 2;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;   // 4 weight rows, 2 rows of x per thread
-    float acc[4][2] = {};
-    for (int k0 = 0; k0 < g.K; k0 += TK) {
-        for (int i = threadIdx.x; i < TN * TK; i += 256) {
-            const int n = i / TK, k = i % TK;
-            float w = 0.0f;
-            if (n0 + n < g.N) {
-                const int64_t row = static_cast<int64_t>(tile_e) * g.N + n0 + n;
-                const int kk = k0 + k, grp = kk / g.group;
-                const uint32_t byte = g.codes[row * (g.K / 2) + kk / 2];
-                const int q = kk & 1 ? byte >> 4 : byte & 15;
-                int z = 8;
-                if (g.zeros != nullptr) {
-                    const uint32_t zb = g.zeros[row * zrow + grp / 2];
-                    z = grp & 1 ? zb >> 4 : zb & 15;
-                }
-                w = static_cast<float>(q - z) * half_bits_to_float(g.scales[row * nb + grp]);
-            }
-            ws[k][n] = w;
-        }
-        for (int i = threadIdx.x; i < TM * TK; i += 256) {
-            const int m = i / TK, k = i % TK;
-            float v = 0.0f;
-            if (m < tile_rows) {
-                const int64_t src = g.rows != nullptr ? g.rows[tile_r0 + m] : tile_r0 + m;
-                if (src >= 0 && src < g.Tx) v = load_x(g, src, k0 + k);
-            }
-            xs[k][m] = v;
-        }
-        __syncthreads();
-#pragma unroll 8
-        for (int k = 0; k < TK; ++k) {
-            const float x0 = xs[k][ty * 2], x1 = xs[k][ty * 2 + 1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float w = ws[k][tx * 4 + i];
-                acc[i][0] = fmaf(w, x0, acc[i][0]);
-                acc[i][1] = fmaf(w, x1, acc[i][1]);
-            }
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        if (ty * 2 + j >= tile_rows) continue;
-        const int64_t r = tile_r0 + ty * 2 + j;
-        const int n = n0 + tx * 4;
-        if (g.swiglu) {
-#pragma unroll
-            for (int i = 0; i < 4; i += 2)
-                if (n + i < g.N) {
-                    const float v = acc[i][j];
-                    store_y(g, r * (g.N / 2) + (n + i) / 2, v / (1.0f + expf(-v)) * acc[i + 1][j]);
-                }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n + i < g.N) store_y(g, r * g.N + n + i, acc[i][j]);
-        }
-    }
+int64_t moe_gemm_workspace_bytes(int64_t R, int64_t Tx, int64_t, int64_t K, int E, bool bf16) {
+    return layout_of(R, Tx, K, E, bf16).total;
 }
 
-int64_t moe_gemm_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int, bool) { return 0; }
-
 int launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t stream) {
-    const int64_t tiles = a.R / TM + (a.E < a.R ? a.E : a.R);   // at most: full tiles, and a partial one per expert
-    if (tiles > 65535) return Q4_ERR_UNSUPPORTED;
-    return launch_overlappable(moe_gemm_kernel, dim3((a.N + TN - 1) / TN, static_cast<unsigned>(tiles)), dim3(256), 0,
-                               stream, call_options().overlap, a);
+    const bool bf16 = a.bf16 != 0;
+    const Layout l = layout_of(a.R, a.Tx, a.K, a.E, bf16);
+    unsigned char *w = static_cast<unsigned char *>(a.workspace);
+    const int ctas = device_info().sms;
+    MoeKernelArgs g;
+    g.scales = a.scales;
+    g.zeros = a.zeros;
+    g.rows = a.rows;
+    g.offsets = a.offsets;
+    g.xscale = reinterpret_cast<float *>(w + l.xscale);
+    g.y = a.y;
+    g.partial = reinterpret_cast<float *>(w + l.partial);
+    g.arrived = reinterpret_cast<unsigned int *>(w + l.arrived);
+    g.E = a.E;
+    g.R = a.R;
+    g.Tx = a.Tx;
+    g.N = a.N;
+    g.K = a.K;
+    g.nb = a.K / a.group;
+    g.zrow = (g.nb + 1) / 2;
+    g.gshift = a.group == 32 ? 5 : (a.group == 64 ? 6 : 7);
+    g.bf16 = a.bf16;
+    g.swiglu = a.swiglu;
+    g.wide_scales = g.nb % 8 == 0 && aligned(a.scales, 16);
+    g.wide_zeros = g.zrow % 8 == 0 && aligned(a.zeros, 8);
+    g.timeout_ns = call_options().wait_ns;
+    g.status = gemm_status_word();
+    g.bounds = bounds_counter();
+    if (g.status == nullptr) return Q4_ERR_CUDA;
+    CUtensorMap codes, x;
+    const int64_t parts = bf16 ? 1 : 2;
+    if (!encode_2d(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, a.K / 2, static_cast<int64_t>(a.E) * a.N, a.K / 2,
+                   kUnit / 2, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_2d(&x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, w, a.K, parts * (static_cast<int64_t>(a.Tx) + 1), 2ll * a.K,
+                   kHalf, 1, CU_TENSOR_MAP_SWIZZLE_128B))
+        return Q4_ERR_UNSUPPORTED;
+    __half *xp = reinterpret_cast<__half *>(w);
+    float *xscale = reinterpret_cast<float *>(w + l.xscale);
+    const dim3 grid(static_cast<unsigned>(a.Tx + 1));
+    const bool overlap = call_options().overlap;
+    int st = bf16 ? launch_overlappable(moe_prepare_kernel<true>, grid, dim3(256), 0, stream, overlap, a.x, a.Tx, a.K,
+                                        xp, xscale, g.arrived, ctas)
+                  : launch_overlappable(moe_prepare_kernel<false>, grid, dim3(256), 0, stream, overlap, a.x, a.Tx, a.K,
+                                        xp, xscale, g.arrived, ctas);
+    if (st != Q4_OK) return st;
+    const Tile t = tile_of(a.R, a.E);
+    if (t.nt == 32)
+        return bf16 ? launch_tile<1, 1, 32>(codes, x, g, stream) : launch_tile<2, 1, 32>(codes, x, g, stream);
+    return bf16 ? launch_tile<1, 2, 128>(codes, x, g, stream) : launch_tile<2, 2, 128>(codes, x, g, stream);
 }
 
 }  // namespace q4
