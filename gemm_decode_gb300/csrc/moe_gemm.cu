@@ -15,6 +15,7 @@ int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 // Workspace: prepared x, its scales, arrival counters, partial sums.
 struct Layout {
     int64_t xscale, arrived, partial, total;
+    int counters;
 };
 
 // Tile: rows of x per item.  One weight tile with 32 rows of x streams the weights with the
@@ -23,15 +24,19 @@ struct Layout {
 struct Tile {
     int rt, nt;
 };
-Tile tile_of(int64_t R, int E) { return R > 24 * static_cast<int64_t>(E) ? Tile{2, 128} : Tile{1, 32}; }
+Tile tile_of(int64_t R, int E, bool bf16) {
+    if (R <= 24 * static_cast<int64_t>(E)) return Tile{1, 32};
+    return bf16 ? Tile{2, 128} : Tile{1, 64};
+}
 
 Layout layout_of(int64_t R, int64_t Tx, int64_t K, int E, bool bf16) {
-    const Tile t = tile_of(R, E);
+    const Tile t = tile_of(R, E, bf16);
     const int64_t ctas = device_info().sms;
     Layout l;
+    l.counters = static_cast<int>(ctas) * t.rt;
     l.xscale = round256((Tx + 1) * K * (bf16 ? 2 : 4));
     l.arrived = l.xscale + round256(4 * (Tx + 1));
-    l.partial = l.arrived + round256(4 * ctas);
+    l.partial = l.arrived + round256(4 * ctas * t.rt);
     l.total = l.partial + 2 * ctas * 4 * t.rt * 128 * t.nt;
     return l;
 }
@@ -49,7 +54,7 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base, int
 }
 
 template <int PARTS, int RT, int NT>
-int launch_tile(const CUtensorMap &codes, const CUtensorMap &x, const MoeKernelArgs &g, cudaStream_t stream) {
+int launch_tile(const CUtensorMap &codes, const MoeKernelArgs &g, cudaStream_t stream) {
     using S = MoeShape<PARTS, RT, NT>;
     auto kern = moe_gemm_kernel<PARTS, RT, NT>;
     static std::atomic<bool> configured[64];
@@ -66,7 +71,7 @@ int launch_tile(const CUtensorMap &codes, const CUtensorMap &x, const MoeKernelA
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
     return launch_overlappable(kern, dim3(static_cast<unsigned>(device_info().sms)), dim3(S::kThreads), S::smem(g.E),
-                               stream, true, codes, x, g);
+                               stream, true, codes, g);
 }
 
 }  // namespace
@@ -77,9 +82,12 @@ int64_t moe_gemm_workspace_bytes(int64_t R, int64_t Tx, int64_t, int64_t K, int 
 
 int launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t stream) {
     const bool bf16 = a.bf16 != 0;
+    const Tile t = tile_of(a.R, a.E, bf16);
+    // items are counted in 32 bits, and so are units while the K of items is shared
+    const int64_t most = (a.R / t.nt + std::min<int64_t>(a.R, a.E)) * ((a.N + 128 * t.rt - 1) / (128 * t.rt));
+    if (most > 0x7fffffffLL || a.K > (1 << 26)) return Q4_ERR_UNSUPPORTED;
     const Layout l = layout_of(a.R, a.Tx, a.K, a.E, bf16);
     unsigned char *w = static_cast<unsigned char *>(a.workspace);
-    const int ctas = device_info().sms;
     MoeKernelArgs g;
     g.scales = a.scales;
     g.zeros = a.zeros;
@@ -97,7 +105,6 @@ int launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t stream) {
     g.nb = a.K / a.group;
     g.zrow = (g.nb + 1) / 2;
     g.gshift = a.group == 32 ? 5 : (a.group == 64 ? 6 : 7);
-    g.bf16 = a.bf16;
     g.swiglu = a.swiglu;
     g.wide_scales = g.nb % 8 == 0 && aligned(a.scales, 16);
     g.wide_zeros = g.zrow % 8 == 0 && aligned(a.zeros, 8);
@@ -105,26 +112,23 @@ int launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t stream) {
     g.status = gemm_status_word();
     g.bounds = bounds_counter();
     if (g.status == nullptr) return Q4_ERR_CUDA;
-    CUtensorMap codes, x;
-    const int64_t parts = bf16 ? 1 : 2;
+    CUtensorMap codes;
     if (!encode_2d(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, a.K / 2, static_cast<int64_t>(a.E) * a.N, a.K / 2,
-                   kUnit / 2, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !encode_2d(&x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, w, a.K, parts * (static_cast<int64_t>(a.Tx) + 1), 2ll * a.K,
-                   kHalf, 1, CU_TENSOR_MAP_SWIZZLE_128B))
+                   kUnit / 2, 128, CU_TENSOR_MAP_SWIZZLE_64B))
         return Q4_ERR_UNSUPPORTED;
     __half *xp = reinterpret_cast<__half *>(w);
+    g.xparts = xp;
     float *xscale = reinterpret_cast<float *>(w + l.xscale);
     const dim3 grid(static_cast<unsigned>(a.Tx + 1));
     const bool overlap = call_options().overlap;
     int st = bf16 ? launch_overlappable(moe_prepare_kernel<true>, grid, dim3(256), 0, stream, overlap, a.x, a.Tx, a.K,
-                                        xp, xscale, g.arrived, ctas)
+                                        xp, xscale, g.arrived, l.counters)
                   : launch_overlappable(moe_prepare_kernel<false>, grid, dim3(256), 0, stream, overlap, a.x, a.Tx, a.K,
-                                        xp, xscale, g.arrived, ctas);
+                                        xp, xscale, g.arrived, l.counters);
     if (st != Q4_OK) return st;
-    const Tile t = tile_of(a.R, a.E);
     if (t.nt == 32)
-        return bf16 ? launch_tile<1, 1, 32>(codes, x, g, stream) : launch_tile<2, 1, 32>(codes, x, g, stream);
-    return bf16 ? launch_tile<1, 2, 128>(codes, x, g, stream) : launch_tile<2, 2, 128>(codes, x, g, stream);
+        return bf16 ? launch_tile<1, 1, 32>(codes, g, stream) : launch_tile<2, 1, 32>(codes, g, stream);
+    return bf16 ? launch_tile<1, 2, 128>(codes, g, stream) : launch_tile<2, 1, 64>(codes, g, stream);
 }
 
 }  // namespace q4

@@ -10,8 +10,12 @@
 // binary32 to 22 bits, whatever the row's range.  (q - z) is exact in binary16 and times s
 // it is rounded once; with two parts the remainder of that rounding is a second binary16
 // number, exactly (the product has 15 bits).  Products are exact and sums binary32 in
-// tensor memory: PARTS = 1 accumulates w x, PARTS = 2 accumulates w_hi x_hi + w_hi x_lo +
-// w_lo x_hi (what is left out is 2^-22 of the product).
+// tensor memory.  PARTS = 1 accumulates w x.  PARTS = 2 accumulates w_hi x_hi in one set of
+// columns and w_hi x_lo + w_lo x_hi in a second (what is left out is 2^-22 of the product);
+// both weights see x_hi and x_lo as adjacent rows of one operand, so the first costs no MMA
+// of its own.  The tensor core cuts what its binary32 sums cannot hold (measured: 2e-8 of
+// the sum per MMA, all in one direction), so with two parts the epilogue takes the sums
+// over every kDrain units and adds them in registers, rounding to nearest.
 //
 // Work.  An item is 128 * RT weight rows by up to NT rows of one expert; its K is cut into
 // units of 128.  When items are many each CTA takes whole items; when the last wave of
@@ -23,14 +27,18 @@
 // One CTA per SM:
 //   warp 0      bulk tensor copies of the codes of a unit (128 * RT rows x 64 bytes) into a
 //               ring, several units ahead: what keeps HBM busy
-//   warp 1      gathers the rows of x (four rows per copy, by index) for each half unit
-//   warp 2      one lane issues the MMAs, operand A from tensor memory
-//   warp 3      loads scales and zero points, 16 groups per row at a time, and leaves them
+//   warp 1      issues the MMAs, operand A from tensor memory: the whole warp walks the
+//               loop and one elected lane issues a unit's MMAs in a row (issued from a
+//               branch on one lane, with a commit after every four, an MMA took 107 cycles;
+//               this way 24, and 16 is what the tensor core needs for up to 32 columns)
+//   warps 2, 3  load scales and zero points, 16 groups per row at a time, and leave them
 //               in shared memory as one word (s, z) per group and row, rows adjacent
-//   warps 4-7   epilogue: tensor memory -> scale, SwiGLU, rounding, store; partial sums
-//   warps 8-    dequantisers, four warps (128 rows) per half unit: a thread owns a row,
-//               reads 32 bytes of codes and writes 64 weights into 32 columns of tensor
-//               memory, where the MMA reads them -- no trip through shared memory
+//   next 4 RT   epilogue, four warps per weight tile: tensor memory -> scale, SwiGLU, rounding, store; partial sums
+//   next 4      copy the rows of x of each unit, by index (16-byte asynchronous copies: a
+//               bulk copy of four rows by index took a lane 80 to 140 cycles to issue)
+//   the rest    dequantisers, four warps (128 rows) per unit and weight tile: a thread owns
+//               a row, reads 64 bytes of codes and writes 128 weights into 64 columns of
+//               tensor memory, where the MMA reads them -- no trip through shared memory
 // A word of eight codes in natural order yields the pairs (0,4), (1,5), (2,6), (3,7) with
 // one logic operation each; the prepared x has its elements in that order.
 //
@@ -40,6 +48,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "q4_moe.cuh"
 #include "q4_tc.cuh"
 
@@ -48,21 +58,23 @@ namespace q4 {
 using namespace tc;
 
 constexpr int kUnit = 128;     // k per unit: 64 bytes of codes per row
-constexpr int kHalf = 64;      // k per MMA stage: 128 bytes of binary16 per row of x
+constexpr int kHalf = 64;      // k per 128 bytes of binary16, a row of the swizzled tile of x
 constexpr int kChunk = 16;     // groups per row that the scale loader brings at a time
-constexpr int kSlotCols = 32;  // tensor-memory columns of 64 weights per lane
+constexpr int kSlotCols = 64;  // tensor-memory columns of 128 weights per lane
+constexpr int kDrain = 2;      // units between the epilogue's additions in registers (PARTS = 2)
 constexpr int kTmemCols = 512;
 
 struct MoeKernelArgs {
     const uint16_t *scales;
     const uint8_t *zeros;
     const int *rows, *offsets;
-    const float *xscale;     // [Tx + 1] 2^-e of each prepared row (row Tx: zeros)
+    const __half *xparts;    // [PARTS][Tx + 1][K] prepared x (row Tx: zeros)
+    const float *xscale;     // [Tx + 1] 2^-e of each prepared row
     void *y;
     float *partial;          // two slots of 128 RT x NT per CTA
-    unsigned int *arrived;   // one counter per CTA, zeroed by the first kernel
+    unsigned int *arrived;   // RT counters per CTA, zeroed by the first kernel
     int E, R, Tx, N, K, nb, zrow, gshift;   // group = 2^gshift
-    int bf16, swiglu;
+    int swiglu;
     int wide_scales, wide_zeros;   // rows of scales / zero points allow 16- / 8-byte loads
     unsigned long long timeout_ns;
     unsigned int *status;
@@ -71,26 +83,49 @@ struct MoeKernelArgs {
 
 template <int PARTS, int RT, int NT>
 struct MoeShape {
-    static constexpr int kGroups = RT == 1 ? 2 : 4;            // dequantiser groups of four warps
-    static constexpr int kWarps = 8 + 4 * kGroups;
+    static_assert(PARTS == 1 || RT == 1, "two parts: the epilogue holds one tile's sums in registers");
+    static constexpr int kGroups = PARTS == 2 && NT > 32 ? 2 : 3;   // dequantiser groups of four warps
+    static constexpr int kXWarp = 4 + 4 * RT;                  // first of the four that copy x
+    static constexpr int kDqWarp = kXWarp + 4;                 // first dequantiser
+    static constexpr int kWarps = kDqWarp + 4 * kGroups;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kAccCols = RT * NT;                   // one accumulator set
-    static constexpr int kAccs = kAccCols <= 128 ? 2 : 1;
+    static constexpr int kAccCols = RT * PARTS * NT;           // one accumulator set
+    static constexpr int kAccs = kAccCols <= 128 ? 2 : 1;      // sets of accumulators
     static constexpr int kSlots = (kTmemCols - kAccs * kAccCols) / kSlotCols;
     static constexpr int kCodeBytes = RT * 128 * (kUnit / 2);
-    static constexpr int kCodeStages = RT == 1 ? 12 : 4;
-    static constexpr int kXBytes = NT * 128 * PARTS;
-    static constexpr int kXStages = NT >= 128 ? (PARTS == 2 ? 3 : 4) : (PARTS == 2 ? 6 : 8);
+    static constexpr int kCodeStages = RT == 2 ? 3 : (NT == 32 ? 10 : 6);
+    // A dequantiser group skips the jobs of the others, and a wait by parity tells a phase
+    // from the one before it only.  So the ring of weights holds a job per group (the job a
+    // group finished last then lies within the ring), and no more units than the codes' ring
+    // (a free slot of weights then proves that the codes' previous use has landed).
+    static constexpr int kJobs = kSlots / PARTS;
+    static_assert(kGroups <= kJobs && kJobs <= RT * kCodeStages, "a parity could be taken for an older phase's");
+    static constexpr int kXHalf = PARTS * NT * 128;            // rows of x, 64 k
+    static constexpr int kXBytes = 2 * kXHalf;
+    static constexpr int kXStages = kXBytes <= 8192 ? 8 : (kXBytes <= 16384 ? 6 : 4);
+    static constexpr int kXAhead = kXStages / 2;   // units whose copies are in flight while one is handed over
     static constexpr int kScaleBytes = kChunk * RT * 128 * 4;
     static constexpr int kScaleBufs = 2;
-    static constexpr int kBars = 2 * (kCodeStages + kXStages + kScaleBufs + kSlots + kAccs) + 1;
+    static constexpr int kBars = 2 * (kCodeStages + kXStages + kScaleBufs + kSlots + kAccs * RT) + 1;
     static constexpr size_t fixed() {
         return 1024 + static_cast<size_t>(kXStages) * kXBytes + static_cast<size_t>(kCodeStages) * kCodeBytes +
-               static_cast<size_t>(kScaleBufs) * kScaleBytes + 8 * kBars + 2 * NT * 4 + 64;
+               static_cast<size_t>(kScaleBufs) * kScaleBytes + 8 * kBars + RT * 2 * NT * 4 + 64;
     }
-    static size_t smem(int E) { return fixed() + 8 * (static_cast<size_t>(E) + 1); }
+    static constexpr size_t smem(int E) { return fixed() + 8 * (static_cast<size_t>(E) + 1); }
 };
 
+// Whether the phase of the given parity is complete, without suspending.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
     asm volatile(
@@ -99,14 +134,9 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
-// Four rows of a two-dimensional tensor, by index, 64 binary16 each, 128-byte swizzled.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int r0, int r1,
-                                            int r2, int r3) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-        : "memory");
+// 16 bytes to shared memory, zeros where there is nothing to read.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
     asm volatile(
@@ -129,6 +159,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float *f) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
 }
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
 __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
 // (a & mask) | magic in one operation
@@ -142,23 +178,24 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t m
 struct MoePlan {
     const int *first_row;   // [E + 1] shared: first row of each expert
     const int *first_tile;  // [E + 1] shared: first tile of rows of each expert
-    int E, row_groups, units;   // tiles of weight rows per expert, units per item
-    int64_t items;
+    uint32_t E, row_groups, units;   // tiles of weight rows per expert, units per item
+    uint32_t items, ctas;   // ctas: CTAs that take part
     bool whole;             // CTAs take whole items
-    int ctas;               // CTAs that take part
-    int64_t at, end;        // units (or items) left to this CTA
+    uint32_t at, end;       // items (whole) or units left to this CTA
 
-    __device__ __forceinline__ int64_t begin_of(int64_t c) const { return items * units * c / ctas; }
+    __device__ __forceinline__ uint32_t begin_of(uint32_t c) const {
+        return static_cast<uint32_t>(static_cast<uint64_t>(items) * units * c / ctas);
+    }
     // the CTA that holds unit u
-    __device__ __forceinline__ int owner(int64_t u) const {
-        return static_cast<int>(((u + 1) * ctas - 1) / (items * units));
+    __device__ __forceinline__ uint32_t owner(uint32_t u) const {
+        return static_cast<uint32_t>((static_cast<uint64_t>(u + 1) * ctas - 1) / (items * units));
     }
 };
 
 struct MoeSegment {
     int expert, group, row0, rows;   // rows [row0, row0 + rows) of the expert's group of rows
     int k0, k1;                      // units
-    int64_t item;
+    uint32_t item;
 };
 
 template <int NT>
@@ -167,18 +204,17 @@ __device__ __forceinline__ bool next_segment(MoePlan &p, MoeSegment &s) {
     if (p.whole) {
         s.item = p.at;
         s.k0 = 0;
-        s.k1 = p.units;
+        s.k1 = static_cast<int>(p.units);
         p.at += p.ctas;
     } else {
         s.item = p.at / p.units;
         s.k0 = static_cast<int>(p.at - s.item * p.units);
-        const int64_t left = p.end - p.at;
-        s.k1 = s.k0 + left < p.units ? s.k0 + static_cast<int>(left) : p.units;
-        p.at += s.k1 - s.k0;
+        s.k1 = static_cast<int>(min(p.units, s.k0 + (p.end - p.at)));
+        p.at += static_cast<uint32_t>(s.k1 - s.k0);
     }
     const int tile = static_cast<int>(s.item / p.row_groups);
-    s.group = static_cast<int>(s.item - static_cast<int64_t>(tile) * p.row_groups);
-    int lo = 0, hi = p.E;   // the expert with first_tile[e] <= tile < first_tile[e + 1]
+    s.group = static_cast<int>(s.item - static_cast<uint32_t>(tile) * p.row_groups);
+    int lo = 0, hi = static_cast<int>(p.E);   // the expert with first_tile[e] <= tile < first_tile[e + 1]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (p.first_tile[mid] <= tile) lo = mid;
@@ -186,8 +222,7 @@ __device__ __forceinline__ bool next_segment(MoePlan &p, MoeSegment &s) {
     }
     s.expert = lo;
     s.row0 = p.first_row[lo] + (tile - p.first_tile[lo]) * NT;
-    const int left = p.first_row[lo + 1] - s.row0;
-    s.rows = left < NT ? left : NT;
+    s.rows = min(p.first_row[lo + 1] - s.row0, NT);
     return true;
 }
 
@@ -281,9 +316,9 @@ __global__ void __launch_bounds__(256) moe_prepare_kernel(const void *x, int Tx,
 
 template <int PARTS, int RT, int NT>
 __global__ void __launch_bounds__(MoeShape<PARTS, RT, NT>::kThreads, 1)
-moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_x,
-                const MoeKernelArgs g) {
+moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKernelArgs g) {
     using S = MoeShape<PARTS, RT, NT>;
+    static_assert(S::smem(kMaxExperts) <= 227 * 1024, "shared memory of one CTA");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -292,14 +327,14 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_cons
     uint32_t *scale_ring = reinterpret_cast<uint32_t *>(code_ring + S::kCodeStages * S::kCodeBytes);
     uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<unsigned char *>(scale_ring) +
                                                   S::kScaleBufs * S::kScaleBytes);
-    float *row_scale = reinterpret_cast<float *>(bars + S::kBars);   // [2][NT]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(row_scale + 2 * NT);
+    float *row_scale = reinterpret_cast<float *>(bars + S::kBars);   // [RT][2][NT]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(row_scale + RT * 2 * NT);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *last_flag = reinterpret_cast<int *>(tmem_slot + 2);
+    int *last_flag = reinterpret_cast<int *>(tmem_slot + 2);         // [RT]
     int *first_row = reinterpret_cast<int *>(tmem_slot + 4);         // [E + 1]
     int *first_tile = first_row + g.E + 1;                           // [E + 1]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(~0u, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const unsigned long long limit = g.timeout_ns;
     auto ib = [&](bool ok) { return q4_in_bounds(ok, g.bounds); };   // bounds-checking builds
 
@@ -315,27 +350,27 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_cons
     auto a_full = [&](int s) { return bar0 + 8u * (kA + s); };
     auto a_empty = [&](int s) { return bar0 + 8u * (kA + S::kSlots + s); };
     auto d_full = [&](int s) { return bar0 + 8u * (kD + s); };
-    auto d_empty = [&](int s) { return bar0 + 8u * (kD + S::kAccs + s); };
+    auto d_empty = [&](int s) { return bar0 + 8u * (kD + S::kAccs * RT + s); };
     const uint32_t done_bar = bar0 + 8u * (S::kBars - 1);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kCodeStages; ++s) {
             mbar_init(code_full(s), 1);
-            mbar_init(code_empty(s), 4 * S::kGroups);
+            mbar_init(code_empty(s), 4 * RT);
         }
         for (int s = 0; s < S::kXStages; ++s) {
-            mbar_init(x_full(s), 1);
+            mbar_init(x_full(s), 4);
             mbar_init(x_empty(s), 1);
         }
         for (int s = 0; s < S::kScaleBufs; ++s) {
-            mbar_init(sc_full(s), 1);
+            mbar_init(sc_full(s), 2);
             mbar_init(sc_empty(s), 4 * S::kGroups);
         }
         for (int s = 0; s < S::kSlots; ++s) {
             mbar_init(a_full(s), 4);
             mbar_init(a_empty(s), 1);
         }
-        for (int s = 0; s < S::kAccs; ++s) {
+        for (int s = 0; s < S::kAccs * RT; ++s) {
             mbar_init(d_full(s), 1);
             mbar_init(d_empty(s), 4);
         }
@@ -343,14 +378,14 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_cons
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 2) {
+    if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         tc_fence_before();
     }
     wait_prior_grid();
-    if (warp == 3) {
+    if (warp == 2) {
         // rows and tiles of each expert: offsets clamped to [0, R] and never falling
         int row_carry = min(max(g.offsets[0], 0), g.R), tile_carry = 0;
         if (lane == 0) {
@@ -385,7 +420,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_cons
     }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
     allow_next_grid();
 
     MoePlan plan;
@@ -394,21 +429,23 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_cons
     plan.E = g.E;
     plan.row_groups = (g.N + 128 * RT - 1) / (128 * RT);
     plan.units = (g.K + kUnit - 1) / kUnit;
-    plan.items = static_cast<int64_t>(first_tile[g.E]) * plan.row_groups;
+    plan.items = static_cast<uint32_t>(first_tile[g.E]) * plan.row_groups;
     {
-        const int64_t ctas = gridDim.x, waves = (plan.items + ctas - 1) / ctas;
-        // whole items when the last wave wastes less than a tenth of the time
-        plan.whole = plan.items > 0 && waves * ctas * 10 <= plan.items * 11;
-        const int64_t units = plan.items * plan.units;
-        plan.ctas = static_cast<int>(plan.whole || units > ctas ? ctas : (units > 0 ? units : 1));
+        const uint32_t ctas = gridDim.x, waves = (plan.items + ctas - 1) / ctas;
+        // whole items when the last wave wastes less than a tenth of the time (always from
+        // eleven waves on, so items * units below stays within 32 bits)
+        plan.whole = plan.items > 0 && static_cast<uint64_t>(waves) * ctas * 10 <= static_cast<uint64_t>(plan.items) * 11;
         if (plan.whole) {
+            plan.ctas = ctas;
             plan.at = blockIdx.x;
             plan.end = plan.items;
-        } else if (static_cast<int>(blockIdx.x) < plan.ctas) {
-            plan.at = plan.begin_of(blockIdx.x);
-            plan.end = plan.begin_of(blockIdx.x + 1);
         } else {
+            plan.ctas = max(1u, min(ctas, plan.items * plan.units));
             plan.at = plan.end = 0;
+            if (blockIdx.x < plan.ctas) {
+                plan.at = plan.begin_of(blockIdx.x);
+                plan.end = plan.begin_of(blockIdx.x + 1);
+            }
         }
     }
     const int per_chunk = (1 << g.gshift) / 8;   // units per chunk of 16 groups
@@ -463,106 +500,131 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_cons
                               static_cast<uint32_t>(j / S::kCodeStages) & 1u, 50ull * 1000 * 1000);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ rows of x
-        Ring<S::kXStages> r;
-        int64_t issued = 0;
+        // ------------------------------------------------------------ MMA
+        Ring<S::kXStages> rx;
+        Ring<S::kSlots> ra;
+        Ring<S::kAccs> rd;
         MoeSegment s;
         bool ok = true;
         while (ok && next_segment<NT>(plan, s)) {
-            const int loads = (s.rows + 15) / 16 * 4;   // copies of four rows, to a multiple of 16
-            int at[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = lane * 4 + i;
-                int src = g.Tx;
-                if (j < s.rows) {
-                    src = g.rows != nullptr ? g.rows[s.row0 + j] : s.row0 + j;
-                    if (src < 0 || src >= g.Tx) src = g.Tx;   // the row of zeros
-                }
-                at[i] = src;
-            }
+            const int n16 = (s.rows + 15) / 16 * 16;
+            const uint32_t idesc = idesc_f16(false, 128, PARTS * n16), idesc_lo = idesc_f16(false, 128, n16);
+            bool fresh = true;   // the accumulators hold nothing of this segment
             for (int u = s.k0; ok && u < s.k1; ++u) {
-                const int halves = halves_of(u);
-                for (int h = 0; h < halves; ++h) {
-                    if (!wait(x_empty(r.s), r.ph ^ 1u)) ok = false;
-                    ok = __all_sync(~0u, ok);
-                    if (!ok) break;
-                    if (lane == 0) mbar_expect_tx(x_full(r.s), static_cast<uint32_t>(loads) * 512u * PARTS);
-                    __syncwarp();
-                    if (lane < loads) {
-#pragma unroll
-                        for (int p = 0; p < PARTS; ++p) {
-                            const int off = p * (g.Tx + 1);
-                            tma_gather4(smem_addr(x_ring + r.s * S::kXBytes + p * NT * 128 + lane * 512), &map_x,
-                                        x_full(r.s), u * kUnit + h * kHalf, at[0] + off, at[1] + off, at[2] + off,
-                                        at[3] + off);
-                        }
-                    }
-                    r.step();
-                    ++issued;
-                }
-            }
-        }
-        if (*abort_flag && lane == 0)
-            for (int64_t j = issued > S::kXStages ? issued - S::kXStages : 0; j < issued; ++j)
-                mbar_wait(x_full(static_cast<int>(j % S::kXStages)), static_cast<uint32_t>(j / S::kXStages) & 1u,
-                          50ull * 1000 * 1000);
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ MMA
-        if (lane == 0) {
-            Ring<S::kXStages> rx;
-            Ring<S::kSlots> ra;
-            Ring<S::kAccs> rd;
-            MoeSegment s;
-            bool ok = true;
-            while (ok && next_segment<NT>(plan, s)) {
-                const uint32_t idesc = idesc_f16(false, 128, (s.rows + 15) / 16 * 16);
-                if (!wait(d_empty(rd.s), rd.ph ^ 1u)) break;
-                tc_fence_after();
                 const uint32_t acc = tmem + static_cast<uint32_t>(rd.s * S::kAccCols);
-                bool first = true;
-                for (int u = s.k0; ok && u < s.k1; ++u) {
-                    const int halves = halves_of(u);
-                    for (int h = 0; ok && h < halves; ++h) {
-                        if (!wait(x_full(rx.s), rx.ph)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t xb = smem_addr(x_ring + rx.s * S::kXBytes);
+                const uint64_t xd = umma_desc(smem_addr(x_ring + rx.s * S::kXBytes));
+                const bool both = halves_of(u) == 2;
+                const bool drain = u + 1 == s.k1 || (PARTS == 2 && (u + 1 - s.k0) % kDrain == 0);
 #pragma unroll
-                        for (int t = 0; t < RT; ++t) {
+                for (int t = 0; t < RT; ++t) {
 #pragma unroll
-                            for (int p = 0; p < PARTS; ++p) {   // weights: rounded, then the remainder
-                                if (!wait(a_full(ra.s), ra.ph)) {
-                                    ok = false;
-                                    break;
-                                }
-                                tc_fence_after();
-                                const uint32_t a = tmem + S::kAccs * S::kAccCols + ra.s * kSlotCols;
-#pragma unroll
-                                for (int q = 0; q < PARTS - p; ++q)   // x: the second part only with the rounded weights
-#pragma unroll
-                                    for (int kk = 0; kk < kHalf / 16; ++kk)
-                                        umma_f16_ts(acc + t * NT, a + kk * 8, umma_desc(xb + q * NT * 128 + kk * 32),
-                                                    idesc, !first || p > 0 || q > 0 || kk > 0 ? 1u : 0u);
-                                umma_commit(a_empty(ra.s));
-                                ra.step();
-                            }
+                    for (int p = 0; p < PARTS; ++p) {   // weights: rounded, then the remainder
+                        // all the barriers of the step are looked at together: one after
+                        // another, each costs the latency of its own round trip
+                        const bool need_x = t == 0 && p == 0, need_d = fresh && p == 0;
+                        const bool ra_ok = mbar_test(a_full(ra.s), ra.ph);
+                        const bool rx_ok = !need_x || mbar_test(x_full(rx.s), rx.ph);
+                        const bool rd_ok = !need_d || mbar_test(d_empty(rd.s * RT + t), rd.ph ^ 1u);
+                        if (!__all_sync(~0u, ra_ok && rx_ok && rd_ok)) {
+                            if (need_d && !wait(d_empty(rd.s * RT + t), rd.ph ^ 1u)) ok = false;
+                            if (need_x && !wait(x_full(rx.s), rx.ph)) ok = false;
+                            if (!wait(a_full(ra.s), ra.ph)) ok = false;
+                            ok = __all_sync(~0u, ok);
                             if (!ok) break;
                         }
-                        if (!ok) break;
-                        first = false;
-                        umma_commit(x_empty(rx.s));
-                        rx.step();
+                        tc_fence_after();
+                        const uint32_t a = tmem + S::kAccs * S::kAccCols + ra.s * kSlotCols;
+                        const uint32_t d = acc + t * NT + (p == 1 ? n16 : 0);
+                        const uint32_t id = p == 1 ? idesc_lo : idesc;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)   // 16 k: 32 bytes of a row of x, 8 columns of weights
+                                umma_f16_ts(d, a + kk * 8, xd + kk * 2, id, p > 0 || kk > 0 || !fresh ? 1u : 0u);
+                            if (both) {
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_f16_ts(d, a + 32 + kk * 8, xd + S::kXHalf / 16 + kk * 2, id, 1u);
+                            }
+                            umma_commit(a_empty(ra.s));
+                            if (t == RT - 1 && p == PARTS - 1) umma_commit(x_empty(rx.s));
+                            if (drain && p == PARTS - 1) umma_commit(d_full(rd.s * RT + t));
+                        }
+                        __syncwarp();
+                        ra.step();
+                    }
+                    if (!ok) break;
+                }
+                rx.step();
+                fresh = drain;
+                if (drain) rd.step();
+            }
+        }
+        if (elect_one()) umma_commit(done_bar);   // every MMA issued (waited for before tensor memory is freed)
+        __syncwarp();
+    } else if (warp >= S::kXWarp && warp < S::kDqWarp) {
+        // ------------------------------------------------------------ rows of x
+        // Eight lanes copy the 128 bytes of a row's 64 k, 16 bytes each, to where the
+        // 128-byte swizzle wants them.  A unit is handed over when its own copies have
+        // landed, S::kXAhead units after they were issued.
+        Ring<S::kXStages> r, ready;
+        int pending = 0;   // units issued and not handed over
+        MoeSegment s;
+        bool ok = true;
+        const int chunk = lane & 7, sub = (warp - S::kXWarp) * 4 + (lane >> 3);   // row sub of every sixteen
+        const uint32_t x_base = smem_addr(x_ring) + sw128_offset(sub, chunk);     // sixteen rows: 2048 bytes
+        auto hand_over = [&]() {
+            fence_proxy_async();   // the copies' writes, for the tensor core
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_full(ready.s));
+            ready.step();
+            --pending;
+        };
+        while (ok && next_segment<NT>(plan, s)) {
+            const int blocks = (s.rows + 15) / 16;   // of sixteen rows
+            // rows sub, sub + 16, ... of the tile: where the next unit's 16 bytes are
+            const __half *at[NT / 16];
+#pragma unroll
+            for (int i = 0; i < NT / 16; ++i) {
+                const int j = i * 16 + sub;
+                int src = g.Tx;   // the row of zeros
+                if (j < s.rows) {
+                    src = g.rows != nullptr ? g.rows[s.row0 + j] : s.row0 + j;
+                    if (src < 0 || src >= g.Tx) src = g.Tx;
+                }
+                at[i] = g.xparts + static_cast<int64_t>(src) * g.K + s.k0 * kUnit + chunk * 8;
+            }
+            const int64_t second = static_cast<int64_t>(g.Tx + 1) * g.K;   // the second part
+            for (int u = s.k0; u < s.k1; ++u) {
+                if (!wait(x_empty(r.s), r.ph ^ 1u)) ok = false;
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                const int k = u * kUnit + chunk * 8;
+                const uint32_t dst = x_base + r.s * S::kXBytes;
+                const bool have0 = k < g.K, have1 = k + kHalf < g.K;
+#pragma unroll
+                for (int i = 0; i < NT / 16; ++i) {
+                    if (i < blocks) {
+#pragma unroll
+                        for (int p = 0; p < PARTS; ++p) {   // the second part's rows follow the first's
+                            const uint32_t to = dst + (p * blocks + i) * 2048;
+                            const __half *from = at[i] + p * second;
+                            copy16(to, have0 ? from : g.xparts, have0);
+                            copy16(to + S::kXHalf, have1 ? from + kHalf : g.xparts, have1);
+                        }
+                        at[i] += kUnit;
                     }
                 }
-                if (!ok) break;
-                umma_commit(d_full(rd.s));
-                rd.step();
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                r.step();
+                if (++pending > S::kXAhead) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(S::kXAhead) : "memory");
+                    hand_over();
+                }
             }
-            umma_commit(done_bar);   // every MMA issued (waited for before tensor memory is freed)
         }
-    } else if (warp == 3) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        while (pending > 0) hand_over();
+    } else if (warp < 4) {
         // ------------------------------------------------------------ scales and zero points
         Ring<S::kScaleBufs> r;
         MoeSegment s;
@@ -575,12 +637,12 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_cons
                 uint32_t *buf = scale_ring + r.s * (S::kScaleBytes / 4);
                 const int g0 = c * kChunk;
 #pragma unroll 1
-                for (int b = 0; b < RT * 4; b += 4) {
-                    uint4 sc[4][2];
-                    uint2 zz[4];
-                    // four rows per lane at a time, all loads in flight together
+                for (int b = (warp & 1) * 2; b < RT * 4; b += 4) {
+                    uint4 sc[2][2];
+                    uint2 zz[2];
+                    // two rows per lane and warp at a time, all loads in flight together
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         const int n = s.group * (128 * RT) + (b + i) * 32 + lane;
                         sc[i][0] = sc[i][1] = make_uint4(0, 0, 0, 0);
                         zz[i] = g.zeros != nullptr ? make_uint2(0, 0) : make_uint2(0x88888888u, 0x88888888u);
@@ -613,7 +675,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_cons
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         const uint32_t w[8] = {sc[i][0].x, sc[i][0].y, sc[i][0].z, sc[i][0].w,
                                                sc[i][1].x, sc[i][1].y, sc[i][1].z, sc[i][1].w};
 #pragma unroll
@@ -629,224 +691,254 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_cons
                 r.step();
             }
         }
-    } else if (warp < 8) {
+    } else if (warp >= 4 && warp < S::kXWarp) {
         // ------------------------------------------------------------ epilogue
-        const int t = threadIdx.x - 128;          // lane of tensor memory: weight row of the tile
+        const int rt = (warp - 4) >> 2;           // weight tile: four warps each
+        const int t = threadIdx.x - 128 * (1 + rt);   // lane of tensor memory: weight row of the tile
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int cols = g.swiglu ? g.N >> 1 : g.N;
-        auto sync4 = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        using Out = typename std::conditional<PARTS == 1, __nv_bfloat16, float>::type;
+        auto sync4 = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + rt) : "memory"); };
         auto all4 = [&](bool v) {   // the same answer for all four warps
             uint32_t r;
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\t"
                 "setp.ne.u32 p, %1, 0;\n\t"
-                "bar.red.and.pred q, 1, 128, p;\n\t"
+                "bar.red.and.pred q, %2, 128, p;\n\t"
                 "selp.u32 %0, 1, 0, q;\n\t}"
                 : "=r"(r)
-                : "r"(static_cast<uint32_t>(v))
+                : "r"(static_cast<uint32_t>(v)), "r"(1 + rt)
                 : "memory");
             return r != 0;
+        };
+        auto put = [&](Out *p, float v, bool have) {
+            if (!have || !ib(p >= static_cast<Out *>(g.y) && p < static_cast<Out *>(g.y) + static_cast<int64_t>(g.R) * cols)) return;
+            if constexpr (PARTS == 1) *p = __float2bfloat16_rn(v);
+            else *p = v;
         };
         Ring<S::kAccs> rd;
         MoeSegment s;
         int buf = 0;
-        auto store = [&](int row, int col, float v) {
-            const int64_t at = static_cast<int64_t>(row) * cols + col;
-            if (!ib(row >= 0 && row < g.R && col < cols)) return;
-            if (g.bf16) static_cast<__nv_bfloat16 *>(g.y)[at] = __float2bfloat16_rn(v);
-            else static_cast<float *>(g.y)[at] = v;
-        };
         // 16 columns (rows of x from j0 on) of weight row n, unscaled sums in v
         auto finish = [&](int n, int j0, const float *v, const float *scale) {
             if (g.swiglu) {
+                // lanes 2i (gate) and 2i + 1 (up) exchange: the even lane takes rows j, the odd one j + 1
+                const int odd = lane & 1;
+                Out *p = static_cast<Out *>(g.y) + static_cast<int64_t>(s.row0 + j0 + odd) * cols + (n >> 1);
+                float h[8];
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
-                    // lanes 2i (gate) and 2i + 1 (up) exchange: the even lane takes row j, the odd one j + 1
-                    const float other = __shfl_xor_sync(~0u, (lane & 1) ? v[j] : v[j + 1], 1);
-                    const int jj = j0 + j + (lane & 1);
-                    if (jj < s.rows && n < g.N) {
-                        const float f = scale[jj];
-                        const float gate = ((lane & 1) ? other : v[j]) * f, up = ((lane & 1) ? v[j + 1] : other) * f;
-                        store(s.row0 + jj, n >> 1, gate / (1.0f + expf(-gate)) * up);
-                    }
+                    const float other = __shfl_xor_sync(~0u, odd ? v[j] : v[j + 1], 1);
+                    const float f = scale[j0 + j + odd];
+                    const float gate = (odd ? other : v[j]) * f, up = (odd ? v[j + 1] : other) * f;
+                    // bfloat16 outputs: the fast exponential and division are off by 2^-20, the rounding by 2^-8
+                    h[j / 2] = PARTS == 1 ? __fdividef(gate, 1.0f + __expf(-gate)) * up : gate / (1.0f + expf(-gate)) * up;
                 }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    put(p + static_cast<int64_t>(2 * j) * cols, h[j], j0 + 2 * j + odd < s.rows && n < g.N);
             } else {
+                Out *p = static_cast<Out *>(g.y) + static_cast<int64_t>(s.row0 + j0) * cols + n;
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    if (j0 + j < s.rows && n < g.N) store(s.row0 + j0 + j, n, v[j] * scale[j0 + j]);
+                    put(p + static_cast<int64_t>(j) * cols, v[j] * scale[j0 + j], j0 + j < s.rows && n < g.N);
             }
         };
         while (next_segment<NT>(plan, s)) {
-            float *scale = row_scale + buf * NT;
+            float *scale = row_scale + (rt * 2 + buf) * NT;
             buf ^= 1;
-            for (int j = t; j < s.rows; j += 128) {
-                int src = g.rows != nullptr ? g.rows[s.row0 + j] : s.row0 + j;
-                if (src < 0 || src >= g.Tx) src = g.Tx;
-                scale[j] = g.xscale[src];
+            for (int j = t; j < NT; j += 128) {
+                float f = 0.0f;
+                if (j < s.rows) {
+                    int src = g.rows != nullptr ? g.rows[s.row0 + j] : s.row0 + j;
+                    if (src < 0 || src >= g.Tx) src = g.Tx;
+                    f = g.xscale[src];
+                }
+                scale[j] = f;
             }
             sync4();
-            if (!all4(wait(d_full(rd.s), rd.ph))) break;
-            tc_fence_after();
-            const uint32_t acc = tmem + lane_base + static_cast<uint32_t>(rd.s * S::kAccCols);
-            const int n0 = s.group * (128 * RT) + t;
-            if (s.k1 - s.k0 == plan.units) {
+            const int n = s.group * (128 * RT) + rt * 128 + t;
+            const bool whole = s.k1 - s.k0 == static_cast<int>(plan.units);
+            // a CTA that holds part of an item's K leaves its sums in a slot of its own
+            const uint32_t u0 = s.item * plan.units;
+            const uint32_t c0 = whole ? 0 : plan.owner(u0), c1 = whole ? 0 : plan.owner(u0 + plan.units - 1);
+            auto slot_of = [&](uint32_t c) {
+                return g.partial + ((2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * RT + rt) * (128 * NT) + t;
+            };
+            float *mine = slot_of(blockIdx.x);
+            auto emit = [&](int j0, const float *v) {
+                if (whole) {
+                    finish(n, j0, v, scale);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j0 + j < s.rows) mine[(j0 + j) * 128] = v[j];
+                }
+            };
+            const uint32_t acc0 = tmem + lane_base + static_cast<uint32_t>(rt * NT);
+            bool ok = true;
+            if constexpr (PARTS == 1) {
+                ok = all4(wait(d_full(rd.s * RT + rt), rd.ph));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = acc0 + static_cast<uint32_t>(rd.s * S::kAccCols);
 #pragma unroll 1
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll 1
-                    for (int j0 = 0; j0 < s.rows; j0 += 16) {
-                        float v[16];
-                        tmem_ld16(acc + rt * NT + j0, v);
-                        finish(n0 + rt * 128, j0, v, scale);
-                    }
+                for (int j0 = 0; j0 < s.rows; j0 += 16) {
+                    float v[16];
+                    tmem_ld16(acc + j0, v);
+                    emit(j0, v);
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(d_empty(rd.s));
+                if (lane == 0) mbar_arrive(d_empty(rd.s * RT + rt));
+                rd.step();
             } else {
-                // this CTA holds part of the item's K: its sums go to a slot of its own
-                const int64_t u0 = s.item * plan.units;
-                const int c0 = plan.owner(u0), c1 = plan.owner(u0 + plan.units - 1);
-                const int64_t slot_floats = static_cast<int64_t>(RT) * 128 * NT;
-                auto slot_of = [&](int c) { return g.partial + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * slot_floats; };
-                float *mine = slot_of(blockIdx.x);
-#pragma unroll 1
-                for (int rt = 0; rt < RT; ++rt)
+                const int n16 = (s.rows + 15) / 16 * 16;
+                float sum[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sum[j] = 0.0f;
+                for (int u = s.k0; u < s.k1; u += kDrain) {
+                    ok = all4(wait(d_full(rd.s), rd.ph));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t acc = acc0 + static_cast<uint32_t>(rd.s * S::kAccCols);
+#pragma unroll
+                    for (int j0 = 0; j0 < NT; j0 += 16)
+                        if (j0 < s.rows) {
+                            float v[16];
+                            tmem_ld16(acc + j0, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[j0 + j] += v[j];
+                            tmem_ld16(acc + n16 + j0, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[j0 + j] += v[j];
+                        }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(d_empty(rd.s));
+                    rd.step();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int j0 = 0; j0 < NT; j0 += 16)
+                    if (j0 < s.rows) emit(j0, sum + j0);
+            }
+            if (!whole) {
+                __threadfence();
+                sync4();
+                if (t == 0)
+                    last_flag[rt] = atomicAdd(g.arrived + c0 * RT + rt, 1u) == c1 - c0;
+                sync4();
+                if (last_flag[rt] != 0) {
+                    __threadfence();
 #pragma unroll 1
                     for (int j0 = 0; j0 < s.rows; j0 += 16) {
                         float v[16];
-                        tmem_ld16(acc + rt * NT + j0, v);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (j0 + j < s.rows) mine[(rt * NT + j0 + j) * 128 + t] = v[j];
-                    }
-                tc_fence_before();
-                __threadfence();
-                sync4();
-                if (lane == 0) mbar_arrive(d_empty(rd.s));
-                if (t == 0) *last_flag = atomicAdd(g.arrived + c0, 1u) == static_cast<unsigned>(c1 - c0);
-                sync4();
-                const bool last = *last_flag != 0;
-                if (last) {
-                    __threadfence();
-#pragma unroll 1
-                    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll 1
-                        for (int j0 = 0; j0 < s.rows; j0 += 16) {
-                            float v[16];
+                        for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+                        for (uint32_t c = c0; c <= c1; ++c) {
+                            const float *p = slot_of(c);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] = 0.0f;
-                            for (int c = c0; c <= c1; ++c) {
-                                const float *p = slot_of(c);
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    if (j0 + j < s.rows) v[j] += __ldcg(p + (rt * NT + j0 + j) * 128 + t);
-                            }
-                            finish(n0 + rt * 128, j0, v, scale);
+                            for (int j = 0; j < 16; ++j)
+                                if (j0 + j < s.rows) v[j] += __ldcg(p + (j0 + j) * 128);
                         }
+                        finish(n, j0, v, scale);
+                    }
                 }
                 sync4();   // last_flag is read before the next item's
             }
-            rd.step();
         }
-    } else {
+    } else if (warp >= S::kDqWarp) {
         // ------------------------------------------------------------ dequantisers
-        const int group_id = (warp - 8) >> 2;
+        const int group_id = (warp - S::kDqWarp) >> 2;
         const int row = (warp & 3) * 32 + lane;   // weight row of the tile = lane of tensor memory
         const uint32_t slots = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + S::kAccs * S::kAccCols;
         Ring<S::kCodeStages> rc;
         Ring<S::kScaleBufs> rs;
         Ring<S::kSlots> ra;
-        int job = 0;   // half units so far, modulo the number of groups
+        int job = 0;   // weight tiles so far, modulo the number of groups
         MoeSegment s;
         bool ok = true;
         while (ok && next_segment<NT>(plan, s)) {
-            for (int u = s.k0; u < s.k1; ++u) {
-                if (u == s.k0 || u % per_chunk == 0) {
+            for (int u = s.k0; ok && u < s.k1; ++u) {
+                if (u == s.k0 || (u & (per_chunk - 1)) == 0) {
                     if (u != s.k0) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(sc_empty(rs.s));
                         rs.step();
                     }
                     if (!wait(sc_full(rs.s), rs.ph)) ok = false;
-                }
-                if (!wait(code_full(rc.s), rc.ph)) ok = false;
-                ok = __all_sync(~0u, ok);
-                if (!ok) break;
-                const uint32_t *sbuf = scale_ring + rs.s * (S::kScaleBytes / 4);
-                const int halves = halves_of(u);
-                for (int h = 0; h < halves; ++h) {
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) {
-                        const bool mine = job == group_id;
-                        if (++job == S::kGroups) job = 0;
-                        if (!mine) {
-#pragma unroll
-                            for (int p = 0; p < PARTS; ++p) ra.step();
-                            continue;
-                        }
-                        const unsigned char *codes = code_ring + rc.s * S::kCodeBytes + t * (128 * kUnit / 2) + row * 64;
-                        const int sw = (row >> 1) & 3;   // 64-byte swizzle: 16-byte chunk c of row r at c ^ ((r >> 1) & 3)
-                        const uint4 c0 = *reinterpret_cast<const uint4 *>(codes + (((2 * h) ^ sw) << 4));
-                        const uint4 c1 = *reinterpret_cast<const uint4 *>(codes + (((2 * h + 1) ^ sw) << 4));
-                        const int k = u * kUnit + h * kHalf;
-                        const int ga = (k >> g.gshift) % kChunk, gb = ((k + 32) >> g.gshift) % kChunk;
-                        const uint32_t sza = sbuf[ga * (128 * RT) + t * 128 + row];
-                        const uint32_t szb = sbuf[gb * (128 * RT) + t * 128 + row];
-                        // slots of this job: the rounded weights, then their remainders
-                        const int sa = ra.s;
-                        const uint32_t pa = ra.ph;
-                        ra.step();
-                        const int sb = ra.s;
-                        const uint32_t pb = ra.ph;
-                        if (PARTS == 2) ra.step();
-                        if (!wait(a_empty(sa), pa ^ 1u)) ok = false;
-                        if (PARTS == 2 && !wait(a_empty(sb), pb ^ 1u)) ok = false;
-                        if (!__all_sync(~0u, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {   // 32 codes of one group
-                            const uint32_t sz = q ? szb : sza;
-                            const uint32_t w4[4] = {q ? c1.x : c0.x, q ? c1.y : c0.y, q ? c1.z : c0.z, q ? c1.w : c0.w};
-                            const __half2 sc = as_half2(__byte_perm(sz, 0, 0x1010));
-                            const uint32_t z = sz >> 16;
-                            const __half2 z0 = as_half2(0x64006400u + z * 0x00010001u);            // 1024 + z
-                            const __half2 z1 = as_half2(0xD400D400u + z * 0x00100010u);            // -(64 + z)
-                            const __half2 sixteenth = as_half2(0x2C002C00u);                       // 1 / 16
-                            uint32_t hi[16], lo[16];
-#pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                const uint32_t a = w4[w], b = a >> 8;
-                                __half2 d[4];
-                                d[0] = __hsub2(as_half2(and_or(a, 0x000F000Fu, 0x64006400u)), z0);
-                                d[1] = __hfma2(as_half2(and_or(a, 0x00F000F0u, 0x64006400u)), sixteenth, z1);
-                                d[2] = __hsub2(as_half2(and_or(b, 0x000F000Fu, 0x64006400u)), z0);
-                                d[3] = __hfma2(as_half2(and_or(b, 0x00F000F0u, 0x64006400u)), sixteenth, z1);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const __half2 v = __hmul2(d[i], sc);
-                                    hi[4 * w + i] = as_u32(v);
-                                    if (PARTS == 2) lo[4 * w + i] = as_u32(__hfma2(d[i], sc, __hneg2(v)));
-                                }
-                            }
-                            tmem_st16(slots + sa * kSlotCols + q * 16, hi);
-                            if (PARTS == 2) tmem_st16(slots + sb * kSlotCols + q * 16, lo);
-                        }
-                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(a_full(sa));
-                            if (PARTS == 2) mbar_arrive(a_full(sb));
-                        }
-                    }
+                    ok = __all_sync(~0u, ok);
                     if (!ok) break;
                 }
-                ok = __all_sync(~0u, ok);
-                if (!ok) break;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(code_empty(rc.s));
+                const uint32_t *sbuf = scale_ring + rs.s * (S::kScaleBytes / 4) + row;
+                const bool both = halves_of(u) == 2;
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const bool mine = job == group_id;
+                    if (++job == S::kGroups) job = 0;
+                    // slots of this job: the rounded weights, then their remainders
+                    const int sa = ra.s;
+                    const uint32_t pa = ra.ph;
+                    ra.step();
+                    const int sb = ra.s;
+                    const uint32_t pb = ra.ph;
+                    if (PARTS == 2) ra.step();
+                    if (!mine) continue;
+                    if (!wait(a_empty(sa), pa ^ 1u)) ok = false;   // before code_full: see MoeShape
+                    if (PARTS == 2 && !wait(a_empty(sb), pb ^ 1u)) ok = false;
+                    if (!wait(code_full(rc.s), rc.ph)) ok = false;
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    // 64-byte swizzle: 16-byte chunk c of row r lies at c ^ ((r >> 1) & 3)
+                    const unsigned char *codes = code_ring + rc.s * S::kCodeBytes + t * (128 * kUnit / 2) + row * 64;
+                    uint4 c4[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        c4[q] = *reinterpret_cast<const uint4 *>(codes + ((q ^ ((row >> 1) & 3)) << 4));
+                    uint32_t sz[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        sz[q] = sbuf[((u * kUnit + q * 32) >> g.gshift) % kChunk * (128 * RT) + t * 128];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {   // 32 codes of one group
+                        if (q >= 2 && !both) break;
+                        const uint32_t w4[4] = {c4[q].x, c4[q].y, c4[q].z, c4[q].w};
+                        const __half2 sc = as_half2(__byte_perm(sz[q], 0, 0x1010));
+                        const uint32_t z = sz[q] >> 16;
+                        const __half2 z0 = as_half2(0x64006400u + z * 0x00010001u);   // 1024 + z
+                        const __half2 z1 = as_half2(0xD400D400u + z * 0x00100010u);   // -(64 + z)
+                        const __half2 sixteenth = as_half2(0x2C002C00u);              // 1 / 16
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t a = w4[w], b = a >> 8;
+                            __half2 d[4];
+                            d[0] = __hsub2(as_half2(and_or(a, 0x000F000Fu, 0x64006400u)), z0);
+                            d[1] = __hfma2(as_half2(and_or(a, 0x00F000F0u, 0x64006400u)), sixteenth, z1);
+                            d[2] = __hsub2(as_half2(and_or(b, 0x000F000Fu, 0x64006400u)), z0);
+                            d[3] = __hfma2(as_half2(and_or(b, 0x00F000F0u, 0x64006400u)), sixteenth, z1);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const __half2 v = __hmul2(d[i], sc);
+                                hi[4 * w + i] = as_u32(v);
+                                if (PARTS == 2) lo[4 * w + i] = as_u32(__hfma2(d[i], sc, __hneg2(v)));
+                            }
+                        }
+                        tmem_st16(slots + sa * kSlotCols + q * 16, hi);
+                        if (PARTS == 2) tmem_st16(slots + sb * kSlotCols + q * 16, lo);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(code_empty(rc.s));
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(a_full(sa));
+                        if (PARTS == 2) mbar_arrive(a_full(sb));
+                    }
+                }
                 rc.step();
             }
             if (!ok) break;
@@ -857,7 +949,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_cons
     }
     // ---- every role is done; MMAs complete before tensor memory is freed ----
     __syncthreads();
-    if (warp == 2) {
+    if (warp == 1) {
         mbar_wait(done_bar, 0, 50ull * 1000 * 1000);
         __syncwarp();
         tc_fence_after();
