@@ -99,17 +99,17 @@ struct MoeShape {
     // group finished last then lies within the ring), and no more units than the codes' ring
     // (a free slot of weights then proves that the codes' previous use has landed).
     static constexpr int kJobs = kSlots / PARTS;
+    static_assert(kSlots % PARTS == 0 && kGroups <= kCodeStages, "whole jobs; a group's next unit within the codes' ring");
     static_assert(kGroups <= kJobs && kJobs <= RT * kCodeStages, "a parity could be taken for an older phase's");
     static constexpr int kXHalf = PARTS * NT * 128;            // rows of x, 64 k
     static constexpr int kXBytes = 2 * kXHalf;
     static constexpr int kXStages = kXBytes <= 8192 ? 8 : (kXBytes <= 16384 ? 6 : 4);
-    static constexpr int kXAhead = kXStages / 2;   // units whose copies are in flight while one is handed over
     static constexpr int kScaleBytes = kChunk * RT * 128 * 4;
     static constexpr int kScaleBufs = 2;
     static constexpr int kBars = 2 * (kCodeStages + kXStages + kScaleBufs + kSlots + kAccs * RT) + 1;
     static constexpr size_t fixed() {
         return 1024 + static_cast<size_t>(kXStages) * kXBytes + static_cast<size_t>(kCodeStages) * kCodeBytes +
-               static_cast<size_t>(kScaleBufs) * kScaleBytes + 8 * kBars + RT * 2 * NT * 4 + 64;
+               static_cast<size_t>(kScaleBufs) * kScaleBytes + 8 * kBars + RT * 2 * NT * 4 + 4 * NT * 4 + 64;
     }
     static constexpr size_t smem(int E) { return fixed() + 8 * (static_cast<size_t>(E) + 1); }
 };
@@ -237,6 +237,13 @@ struct Ring {
             ph ^= 1u;
         }
     }
+    __device__ __forceinline__ void step(int n) {   // n <= STAGES
+        s += n;
+        if (s >= STAGES) {
+            s -= STAGES;
+            ph ^= 1u;
+        }
+    }
 };
 
 // The parts of x, scaled by a power of two per row, elements permuted within eights;
@@ -328,7 +335,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKernelAr
     uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<unsigned char *>(scale_ring) +
                                                   S::kScaleBufs * S::kScaleBytes);
     float *row_scale = reinterpret_cast<float *>(bars + S::kBars);   // [RT][2][NT]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(row_scale + RT * 2 * NT);
+    int *x_rows = reinterpret_cast<int *>(row_scale + RT * 2 * NT);  // [4][NT] rows of x, a list per copying warp
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(x_rows + 4 * NT);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *last_flag = reinterpret_cast<int *>(tmem_slot + 2);         // [RT]
     int *first_row = reinterpret_cast<int *>(tmem_slot + 4);         // [E + 1]
@@ -359,7 +367,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKernelAr
             mbar_init(code_empty(s), 4 * RT);
         }
         for (int s = 0; s < S::kXStages; ++s) {
-            mbar_init(x_full(s), 4);
+            mbar_init(x_full(s), 1);
             mbar_init(x_empty(s), 1);
         }
         for (int s = 0; s < S::kScaleBufs; ++s) {
@@ -448,7 +456,6 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKernelAr
             }
         }
     }
-    const int per_chunk = (1 << g.gshift) / 8;   // units per chunk of 16 groups
 
     auto fail = [&]() {
         *abort_flag = 1;
@@ -460,15 +467,13 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKernelAr
         if (limit != 0) {
             const unsigned long long t0 = global_ns();
             for (;;) {
-                for (int i = 0; i < 16; ++i)
-                    if (mbar_try(bar, parity)) return true;
+                if (mbar_try_sleep(bar, parity, 20000u)) return true;
                 if (*abort_flag || global_ns() - t0 > limit) break;
             }
         }
         fail();
         return false;
     };
-    auto halves_of = [&](int u) { return g.K - u * kUnit > kHalf ? 2 : 1; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ codes
@@ -506,14 +511,16 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKernelAr
         Ring<S::kAccs> rd;
         MoeSegment s;
         bool ok = true;
+        const uint64_t x_desc = umma_desc(smem_addr(x_ring));
         while (ok && next_segment<NT>(plan, s)) {
             const int n16 = (s.rows + 15) / 16 * 16;
             const uint32_t idesc = idesc_f16(false, 128, PARTS * n16), idesc_lo = idesc_f16(false, 128, n16);
             bool fresh = true;   // the accumulators hold nothing of this segment
+            const int half_unit = g.K % kUnit != 0 && g.K % kUnit <= kHalf ? g.K / kUnit : -1;   // the unit of one half
             for (int u = s.k0; ok && u < s.k1; ++u) {
                 const uint32_t acc = tmem + static_cast<uint32_t>(rd.s * S::kAccCols);
-                const uint64_t xd = umma_desc(smem_addr(x_ring + rx.s * S::kXBytes));
-                const bool both = halves_of(u) == 2;
+                const uint64_t xd = x_desc + static_cast<uint32_t>(rx.s) * (S::kXBytes / 16);
+                const bool both = u != half_unit;
                 const bool drain = u + 1 == s.k1 || (PARTS == 2 && (u + 1 - s.k0) % kDrain == 0);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
@@ -563,74 +570,89 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKernelAr
         __syncwarp();
     } else if (warp >= S::kXWarp && warp < S::kDqWarp) {
         // ------------------------------------------------------------ rows of x
-        // Eight lanes copy the 128 bytes of a row's 64 k, 16 bytes each, to where the
-        // 128-byte swizzle wants them.  A unit is handed over when its own copies have
-        // landed, S::kXAhead units after they were issued.
-        Ring<S::kXStages> r, ready;
-        int pending = 0;   // units issued and not handed over
+        // The four warps take the units in turn.  Eight lanes copy the 128 bytes of a row's
+        // 64 k, 16 bytes each, to where the 128-byte swizzle wants them.  A unit is handed
+        // over when its copies have landed: after the warp's next unit has been issued if
+        // there is room for that already, else before the warp waits for room.
+        const int me = warp - S::kXWarp;
+        Ring<S::kXStages> r;
+        r.step(me % S::kXStages);
+        int full = -1;     // stage whose copies are in flight
+        uint32_t next = static_cast<uint32_t>(me), before = 0;   // the warp's next unit; units of earlier segments
         MoeSegment s;
         bool ok = true;
-        const int chunk = lane & 7, sub = (warp - S::kXWarp) * 4 + (lane >> 3);   // row sub of every sixteen
-        const uint32_t x_base = smem_addr(x_ring) + sw128_offset(sub, chunk);     // sixteen rows: 2048 bytes
+        const int chunk = lane & 7, sub = lane >> 3;
+        const uint32_t x_base = smem_addr(x_ring);
+        int *list = x_rows + me * NT;
         auto hand_over = [&]() {
             fence_proxy_async();   // the copies' writes, for the tensor core
             __syncwarp();
-            if (lane == 0) mbar_arrive(x_full(ready.s));
-            ready.step();
-            --pending;
+            if (lane == 0) mbar_arrive(x_full(full));
         };
         while (ok && next_segment<NT>(plan, s)) {
-            const int blocks = (s.rows + 15) / 16;   // of sixteen rows
-            // rows sub, sub + 16, ... of the tile: where the next unit's 16 bytes are
-            const __half *at[NT / 16];
-#pragma unroll
-            for (int i = 0; i < NT / 16; ++i) {
-                const int j = i * 16 + sub;
+            const uint32_t units = static_cast<uint32_t>(s.k1 - s.k0);
+            if (next - before >= units) {   // none of this segment's units is this warp's
+                before += units;
+                continue;
+            }
+            const int n16 = (s.rows + 15) & ~15;
+            __syncwarp();
+            for (int j = lane; j < n16; j += 32) {
                 int src = g.Tx;   // the row of zeros
                 if (j < s.rows) {
                     src = g.rows != nullptr ? g.rows[s.row0 + j] : s.row0 + j;
                     if (src < 0 || src >= g.Tx) src = g.Tx;
                 }
-                at[i] = g.xparts + static_cast<int64_t>(src) * g.K + s.k0 * kUnit + chunk * 8;
+                list[j] = src;
             }
-            const int64_t second = static_cast<int64_t>(g.Tx + 1) * g.K;   // the second part
-            for (int u = s.k0; u < s.k1; ++u) {
-                if (!wait(x_empty(r.s), r.ph ^ 1u)) ok = false;
-                ok = __all_sync(~0u, ok);
-                if (!ok) break;
+            __syncwarp();
+            for (; next - before < units; next += 4) {
+                const int u = s.k0 + static_cast<int>(next - before);
+                if (!__all_sync(~0u, mbar_test(x_empty(r.s), r.ph ^ 1u))) {
+                    if (full >= 0) {
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                        hand_over();
+                        full = -1;
+                    }
+                    if (!wait(x_empty(r.s), r.ph ^ 1u)) ok = false;
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                }
                 const int k = u * kUnit + chunk * 8;
                 const uint32_t dst = x_base + r.s * S::kXBytes;
                 const bool have0 = k < g.K, have1 = k + kHalf < g.K;
+                const __half *from = g.xparts + (have0 ? k : 0);
+#pragma unroll 4
+                for (int j = sub; j < n16; j += 4) {
+                    const __half *row = from + static_cast<int64_t>(list[j]) * g.K;
 #pragma unroll
-                for (int i = 0; i < NT / 16; ++i) {
-                    if (i < blocks) {
-#pragma unroll
-                        for (int p = 0; p < PARTS; ++p) {   // the second part's rows follow the first's
-                            const uint32_t to = dst + (p * blocks + i) * 2048;
-                            const __half *from = at[i] + p * second;
-                            copy16(to, have0 ? from : g.xparts, have0);
-                            copy16(to + S::kXHalf, have1 ? from + kHalf : g.xparts, have1);
-                        }
-                        at[i] += kUnit;
+                    for (int p = 0; p < PARTS; ++p) {   // the second part's rows follow the first's
+                        const uint32_t to = dst + sw128_offset(p * n16 + j, chunk);
+                        copy16(to, row, have0);
+                        copy16(to + S::kXHalf, row + (have1 ? kHalf : 0), have1);
+                        row += static_cast<int64_t>(g.Tx + 1) * g.K;
                     }
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
-                r.step();
-                if (++pending > S::kXAhead) {
-                    asm volatile("cp.async.wait_group %0;" ::"n"(S::kXAhead) : "memory");
+                if (full >= 0) {
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
                     hand_over();
                 }
+                full = r.s;
+                if constexpr (S::kXStages == 4) r.ph ^= 1u;
+                else r.step(4);
             }
+            before += units;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        while (pending > 0) hand_over();
+        if (full >= 0) hand_over();
     } else if (warp < 4) {
         // ------------------------------------------------------------ scales and zero points
         Ring<S::kScaleBufs> r;
         MoeSegment s;
         bool ok = true;
         while (ok && next_segment<NT>(plan, s)) {
-            for (int c = s.k0 / per_chunk; c <= (s.k1 - 1) / per_chunk; ++c) {
+            for (int c = s.k0 >> (g.gshift - 3); c <= (s.k1 - 1) >> (g.gshift - 3); ++c) {   // 2^(gshift - 3) units each
                 if (!wait(sc_empty(r.s), r.ph ^ 1u)) ok = false;
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
@@ -853,99 +875,106 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKernelAr
         const int group_id = (warp - S::kDqWarp) >> 2;
         const int row = (warp & 3) * 32 + lane;   // weight row of the tile = lane of tensor memory
         const uint32_t slots = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + S::kAccs * S::kAccCols;
+        // Jobs are (unit, weight tile) in the order the MMAs take them; this group takes every
+        // kGroups-th, whatever segment it falls into.
+        constexpr int G = S::kGroups;
         Ring<S::kCodeStages> rc;
         Ring<S::kScaleBufs> rs;
         Ring<S::kSlots> ra;
-        int job = 0;   // weight tiles so far, modulo the number of groups
+        ra.step(group_id * PARTS);
+        uint32_t next = static_cast<uint32_t>(group_id), before = 0;   // the next job; jobs of earlier segments
+        uint32_t chunk = 0, held = 0;                                  // chunks of earlier segments; chunks taken so far
+        uint32_t unit_at = 0;                                          // unit whose codes are at rc
         MoeSegment s;
         bool ok = true;
-        while (ok && next_segment<NT>(plan, s)) {
-            for (int u = s.k0; ok && u < s.k1; ++u) {
-                if (u == s.k0 || (u & (per_chunk - 1)) == 0) {
-                    if (u != s.k0) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(sc_empty(rs.s));
-                        rs.step();
-                    }
-                    if (!wait(sc_full(rs.s), rs.ph)) ok = false;
-                    ok = __all_sync(~0u, ok);
-                    if (!ok) break;
-                }
-                const uint32_t *sbuf = scale_ring + rs.s * (S::kScaleBytes / 4) + row;
-                const bool both = halves_of(u) == 2;
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const bool mine = job == group_id;
-                    if (++job == S::kGroups) job = 0;
-                    // slots of this job: the rounded weights, then their remainders
-                    const int sa = ra.s;
-                    const uint32_t pa = ra.ph;
-                    ra.step();
-                    const int sb = ra.s;
-                    const uint32_t pb = ra.ph;
-                    if (PARTS == 2) ra.step();
-                    if (!mine) continue;
-                    if (!wait(a_empty(sa), pa ^ 1u)) ok = false;   // before code_full: see MoeShape
-                    if (PARTS == 2 && !wait(a_empty(sb), pb ^ 1u)) ok = false;
-                    if (!wait(code_full(rc.s), rc.ph)) ok = false;
-                    ok = __all_sync(~0u, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                    // 64-byte swizzle: 16-byte chunk c of row r lies at c ^ ((r >> 1) & 3)
-                    const unsigned char *codes = code_ring + rc.s * S::kCodeBytes + t * (128 * kUnit / 2) + row * 64;
-                    uint4 c4[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        c4[q] = *reinterpret_cast<const uint4 *>(codes + ((q ^ ((row >> 1) & 3)) << 4));
-                    uint32_t sz[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        sz[q] = sbuf[((u * kUnit + q * 32) >> g.gshift) % kChunk * (128 * RT) + t * 128];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {   // 32 codes of one group
-                        if (q >= 2 && !both) break;
-                        const uint32_t w4[4] = {c4[q].x, c4[q].y, c4[q].z, c4[q].w};
-                        const __half2 sc = as_half2(__byte_perm(sz[q], 0, 0x1010));
-                        const uint32_t z = sz[q] >> 16;
-                        const __half2 z0 = as_half2(0x64006400u + z * 0x00010001u);   // 1024 + z
-                        const __half2 z1 = as_half2(0xD400D400u + z * 0x00100010u);   // -(64 + z)
-                        const __half2 sixteenth = as_half2(0x2C002C00u);              // 1 / 16
-                        uint32_t hi[16], lo[16];
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t a = w4[w], b = a >> 8;
-                            __half2 d[4];
-                            d[0] = __hsub2(as_half2(and_or(a, 0x000F000Fu, 0x64006400u)), z0);
-                            d[1] = __hfma2(as_half2(and_or(a, 0x00F000F0u, 0x64006400u)), sixteenth, z1);
-                            d[2] = __hsub2(as_half2(and_or(b, 0x000F000Fu, 0x64006400u)), z0);
-                            d[3] = __hfma2(as_half2(and_or(b, 0x00F000F0u, 0x64006400u)), sixteenth, z1);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const __half2 v = __hmul2(d[i], sc);
-                                hi[4 * w + i] = as_u32(v);
-                                if (PARTS == 2) lo[4 * w + i] = as_u32(__hfma2(d[i], sc, __hneg2(v)));
-                            }
-                        }
-                        tmem_st16(slots + sa * kSlotCols + q * 16, hi);
-                        if (PARTS == 2) tmem_st16(slots + sb * kSlotCols + q * 16, lo);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(code_empty(rc.s));
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(a_full(sa));
-                        if (PARTS == 2) mbar_arrive(a_full(sb));
-                    }
-                }
-                rc.step();
+        const int chunk_shift = g.gshift - 3;
+        const int half_unit = g.K % kUnit != 0 && g.K % kUnit <= kHalf ? g.K / kUnit : -1;   // the unit of one half
+        const int swz = (row >> 1) & 3;   // 64-byte swizzle: 16-byte chunk c of row r lies at c ^ ((r >> 1) & 3)
+        auto take_chunk = [&]() {   // let go of the chunk held and wait for the next
+            if (held > 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sc_empty(rs.s));
+                rs.step();
             }
-            if (!ok) break;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sc_empty(rs.s));
-            rs.step();
+            ++held;
+            if (!wait(sc_full(rs.s), rs.ph)) ok = false;
+            ok = __all_sync(~0u, ok);
+        };
+        while (ok && next_segment<NT>(plan, s)) {
+            const uint32_t jobs = static_cast<uint32_t>(s.k1 - s.k0) * RT;
+            const int first_chunk = s.k0 >> chunk_shift;
+            for (; next - before < jobs; next += G) {
+                const int t = RT == 1 ? 0 : static_cast<int>((next - before) % RT);
+                const int u = s.k0 + static_cast<int>((next - before) / RT);
+                // the chunk of scales: every group passes through every chunk
+                const uint32_t want = chunk + static_cast<uint32_t>((u >> chunk_shift) - first_chunk) + 1;
+                while (ok && held < want) take_chunk();
+                if (!ok) break;
+                const uint32_t unit = next / RT;
+                rc.step(static_cast<int>(unit - unit_at));
+                unit_at = unit;
+                // slots of this job: the rounded weights, then their remainders
+                const int sa = ra.s, sb = ra.s + 1;   // kSlots is a multiple of PARTS
+                if (!wait(a_empty(sa), ra.ph ^ 1u)) ok = false;   // before code_full: see MoeShape
+                if (PARTS == 2 && !wait(a_empty(sb), ra.ph ^ 1u)) ok = false;
+                if (!wait(code_full(rc.s), rc.ph)) ok = false;
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                ra.step(G * PARTS);
+                const uint32_t *sbuf = scale_ring + rs.s * (S::kScaleBytes / 4) + row;
+                const bool both = u != half_unit;
+                tc_fence_after();
+                const unsigned char *codes = code_ring + rc.s * S::kCodeBytes + t * (128 * kUnit / 2) + row * 64;
+                uint4 c4[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    c4[q] = *reinterpret_cast<const uint4 *>(codes + ((q ^ swz) << 4));
+                uint32_t sz[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    sz[q] = sbuf[((u * kUnit + q * 32) >> g.gshift) % kChunk * (128 * RT) + t * 128];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {   // 32 codes of one group
+                    if (q >= 2 && !both) break;
+                    const uint32_t w4[4] = {c4[q].x, c4[q].y, c4[q].z, c4[q].w};
+                    const __half2 sc = as_half2(__byte_perm(sz[q], 0, 0x1010));
+                    const uint32_t z = sz[q] >> 16;
+                    const __half2 z0 = as_half2(0x64006400u + z * 0x00010001u);   // 1024 + z
+                    const __half2 z1 = as_half2(0xD400D400u + z * 0x00100010u);   // -(64 + z)
+                    const __half2 sixteenth = as_half2(0x2C002C00u);              // 1 / 16
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t a = w4[w], b = a >> 8;
+                        __half2 d[4];
+                        d[0] = __hsub2(as_half2(and_or(a, 0x000F000Fu, 0x64006400u)), z0);
+                        d[1] = __hfma2(as_half2(and_or(a, 0x00F000F0u, 0x64006400u)), sixteenth, z1);
+                        d[2] = __hsub2(as_half2(and_or(b, 0x000F000Fu, 0x64006400u)), z0);
+                        d[3] = __hfma2(as_half2(and_or(b, 0x00F000F0u, 0x64006400u)), sixteenth, z1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __half2 v = __hmul2(d[i], sc);
+                            hi[4 * w + i] = as_u32(v);
+                            if (PARTS == 2) lo[4 * w + i] = as_u32(__hfma2(d[i], sc, __hneg2(v)));
+                        }
+                    }
+                    tmem_st16(slots + sa * kSlotCols + q * 16, hi);
+                    if (PARTS == 2) tmem_st16(slots + sb * kSlotCols + q * 16, lo);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(code_empty(rc.s));
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(a_full(sa));
+                    if (PARTS == 2) mbar_arrive(a_full(sb));
+                }
+            }
+            before += jobs;
+            chunk += static_cast<uint32_t>(((s.k1 - 1) >> chunk_shift) - first_chunk) + 1;
         }
+        while (ok && held < chunk) take_chunk();   // the other groups need the chunks after this group's last
     }
     // ---- every role is done; MMAs complete before tensor memory is freed ----
     __syncthreads();
