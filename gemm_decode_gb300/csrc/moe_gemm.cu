@@ -1,8 +1,9 @@
-// moe_gemm.cu -- host side of the matrix product grouped by expert (moe_gemm_kernel.cuh):
-// workspace, tensor maps, choice of the tile, launches.
+// moe_gemm.cu -- host side of the matrix product grouped by expert: workspace, tensor map,
+// choice of the kernel (moe_gemm_few.cuh, moe_gemm_many.cuh) and its tile, launches.
 #include <algorithm>
 
-#include "moe_gemm_kernel.cuh"
+#include "moe_gemm_few.cuh"
+#include "moe_gemm_many.cuh"
 
 namespace q4 {
 
@@ -18,19 +19,21 @@ struct Layout {
     int counters;
 };
 
-// Tile: rows of x per item.  One weight tile with 32 rows of x streams the weights with the
-// most copies in flight; 256 weight rows by 128 rows of x read each row of x for twice as
-// many products.
+// Tile: weight tiles and rows of x per item.
+//   bfloat16: up to 24 rows per expert on average, 32 rows of the kernel for few rows; above,
+//   the kernel for many.
+//   binary32: always the kernel for few rows, whose sums per group of weights leave room for
+//   16, 32 or 64 rows with groups of 32, 64 or 128; no more than the average expert fills.
 struct Tile {
     int rt, nt;
 };
-Tile tile_of(int64_t R, int E, bool bf16) {
-    if (R <= 24 * static_cast<int64_t>(E)) return Tile{1, 32};
-    return bf16 ? Tile{2, 128} : Tile{1, 64};
+Tile tile_of(int64_t R, int E, int group, bool bf16) {
+    if (bf16) return R <= 24 * static_cast<int64_t>(E) ? Tile{1, 32} : Tile{2, 128};
+    if (group == 32 || R <= 8 * static_cast<int64_t>(E)) return Tile{1, 16};
+    return group == 64 || R <= 24 * static_cast<int64_t>(E) ? Tile{1, 32} : Tile{1, 64};
 }
 
-Layout layout_of(int64_t R, int64_t Tx, int64_t K, int E, bool bf16) {
-    const Tile t = tile_of(R, E, bf16);
+Layout layout_of(int64_t R, int64_t Tx, int64_t K, const Tile &t, bool bf16) {
     const int64_t ctas = device_info().sms;
     Layout l;
     l.counters = static_cast<int>(ctas) * t.rt;
@@ -53,16 +56,15 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base, int
                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int PARTS, int RT, int NT>
-int launch_tile(const CUtensorMap &codes, const MoeKernelArgs &g, cudaStream_t stream) {
-    using S = MoeShape<PARTS, RT, NT>;
-    auto kern = moe_gemm_kernel<PARTS, RT, NT>;
-    static std::atomic<bool> configured[64];
+// One CTA per SM, overlapped with the kernel that prepares x.
+int launch_product(void (*kern)(CUtensorMap, MoeKernelArgs), int threads, size_t smem, size_t most,
+                   std::atomic<bool> *configured, const CUtensorMap &codes, const MoeKernelArgs &g,
+                   cudaStream_t stream) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !configured[dev]) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(S::smem(kMaxExperts)));
+                                                   static_cast<int>(most));
         if (e != cudaSuccess) {
             cudaGetLastError();
             set_cuda_error(e);
@@ -70,23 +72,39 @@ int launch_tile(const CUtensorMap &codes, const MoeKernelArgs &g, cudaStream_t s
         }
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
-    return launch_overlappable(kern, dim3(static_cast<unsigned>(device_info().sms)), dim3(S::kThreads), S::smem(g.E),
-                               stream, true, codes, g);
+    return launch_overlappable(kern, dim3(static_cast<unsigned>(device_info().sms)),
+                               dim3(static_cast<unsigned>(threads)), smem, stream, true, codes, g);
+}
+template <int PARTS, int NT>
+int launch_few(const CUtensorMap &codes, const MoeKernelArgs &g, cudaStream_t stream) {
+    using S = FewShape<PARTS, NT>;
+    static std::atomic<bool> configured[64];
+    return launch_product(moe_gemm_few_kernel<PARTS, NT>, S::kThreads, S::smem(g.E), S::smem(kMaxExperts), configured,
+                          codes, g, stream);
+}
+int launch_many(const CUtensorMap &codes, const MoeKernelArgs &g, cudaStream_t stream) {
+    using S = ManyShape;
+    static std::atomic<bool> configured[64];
+    return launch_product(moe_gemm_many_kernel, S::kThreads, S::smem(g.E), S::smem(kMaxExperts), configured, codes, g,
+                          stream);
 }
 
 }  // namespace
 
 int64_t moe_gemm_workspace_bytes(int64_t R, int64_t Tx, int64_t, int64_t K, int E, bool bf16) {
-    return layout_of(R, Tx, K, E, bf16).total;
+    int64_t most = 0;   // whatever the group
+    for (int group : {32, 64, 128})
+        most = std::max(most, layout_of(R, Tx, K, tile_of(R, E, group, bf16), bf16).total);
+    return most;
 }
 
 int launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t stream) {
     const bool bf16 = a.bf16 != 0;
-    const Tile t = tile_of(a.R, a.E, bf16);
+    const Tile t = tile_of(a.R, a.E, a.group, bf16);
     // items are counted in 32 bits, and so are units while the K of items is shared
     const int64_t most = (a.R / t.nt + std::min<int64_t>(a.R, a.E)) * ((a.N + 128 * t.rt - 1) / (128 * t.rt));
     if (most > 0x7fffffffLL || a.K > (1 << 26)) return Q4_ERR_UNSUPPORTED;
-    const Layout l = layout_of(a.R, a.Tx, a.K, a.E, bf16);
+    const Layout l = layout_of(a.R, a.Tx, a.K, t, bf16);
     unsigned char *w = static_cast<unsigned char *>(a.workspace);
     MoeKernelArgs g;
     g.scales = a.scales;
@@ -126,9 +144,9 @@ int launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t stream) {
                   : launch_overlappable(moe_prepare_kernel<false>, grid, dim3(256), 0, stream, overlap, a.x, a.Tx, a.K,
                                         xp, xscale, g.arrived, l.counters);
     if (st != Q4_OK) return st;
-    if (t.nt == 32)
-        return bf16 ? launch_tile<1, 1, 32>(codes, g, stream) : launch_tile<2, 1, 32>(codes, g, stream);
-    return bf16 ? launch_tile<1, 2, 128>(codes, g, stream) : launch_tile<2, 1, 64>(codes, g, stream);
+    if (bf16) return t.rt == 1 ? launch_few<1, 32>(codes, g, stream) : launch_many(codes, g, stream);
+    if (t.nt == 16) return launch_few<2, 16>(codes, g, stream);
+    return t.nt == 32 ? launch_few<2, 32>(codes, g, stream) : launch_few<2, 64>(codes, g, stream);
 }
 
 }  // namespace q4
