@@ -8,7 +8,7 @@
 // cuts what its binary32 sums cannot hold (measured: 2e-8 of the sum per MMA, all in one
 // direction); here it adds up no more than eight times.
 //
-// One CTA per SM, 24 warps.  Unit n of the CTA's sequence of units:
+// One CTA per SM, 28 warps (24 with 64 rows of x).  Unit n of the CTA's sequence of units:
 //   warp 0       bulk tensor copy of its codes (128 rows x 64 bytes) into a ring, several
 //                units ahead: what keeps HBM busy
 //   warp 1       its MMAs: the whole warp walks the loop and one elected lane issues them in
@@ -22,7 +22,7 @@
 //                and stores
 //   warps 12-15  copy the rows of x, by index, one unit each in turn (16-byte asynchronous
 //                copies: a bulk copy of four rows by index took a lane 80 to 140 cycles)
-//   warps 16-23  dequantisers, two groups of four warps taking the units in turn: a thread
+//   the rest     dequantisers, three groups (two with 64 rows of x) of four warps taking the units in turn: a thread
 //                owns a weight row, reads 64 bytes of codes and writes 128 weights into 64
 //                columns of tensor memory
 // Two barriers per unit tie them together: ready[n] (weights written, rows of x landed, the
@@ -40,17 +40,22 @@ namespace q4 {
 
 template <int PARTS, int NT>
 struct FewShape {
-    static constexpr int kDq = 2, kEpi = 2;                    // groups of dequantisers, of the epilogue
+    // groups of dequantisers (64 rows of x: two, for the registers), of the epilogue
+    static constexpr int kDq = NT == 64 ? 2 : 3, kEpi = 2;
     static constexpr int kEpiWarp = 4, kXWarp = 12, kDqWarp = 16;
-    static constexpr int kThreads = 768;
+    static constexpr int kFours = 4 + kDq;                     // groups of four warps
+    static constexpr int kThreads = 128 * kFours;
     // registers per thread: what the launch gives, and the roles' shares
-    static constexpr int kRegLaunch = 80, kRegMisc = 72, kRegCopy = 56, kRegDq = 72;
-    static constexpr int kRegSums = (6 * kRegLaunch - kRegMisc - kRegCopy - kDq * kRegDq) / kEpi / 8 * 8;
-    static_assert(kRegMisc + kRegCopy + kDq * kRegDq + kEpi * kRegSums <= 6 * kRegLaunch, "more than the launch has");
-    static constexpr int kPerSet = 128 / (PARTS * NT);         // groups that a set of accumulators holds
-    static constexpr int kAccCols = 128, kAccs = 2;            // one set per epilogue group
+    static constexpr int kRegLaunch = 65536 / kThreads / 8 * 8, kRegMisc = 64, kRegCopy = 48, kRegDq = 64;
+    static constexpr int kRegSums = (kFours * kRegLaunch - kRegMisc - kRegCopy - kDq * kRegDq) / kEpi / 8 * 8;
+    static_assert(kRegMisc + kRegCopy + kDq * kRegDq + kEpi * kRegSums <= kFours * kRegLaunch, "more than the launch has");
+    // Accumulators: half of tensor memory, as sets of one unit's sums (its groups of weights
+    // times the columns of a group); at least two, one per epilogue group, and up to eight,
+    // which the MMAs fill while the epilogue finishes an item.
+    static constexpr int kAccCols = 256;
+    static constexpr int kMostGroups = kAccCols / 2 / (PARTS * NT);   // of a unit
     static constexpr int kSlots = 4;                           // units of weights
-    static_assert(kAccs * kAccCols + kSlots * kSlotCols <= kTmemCols, "tensor memory");
+    static_assert(kAccCols + kSlots * kSlotCols <= kTmemCols, "tensor memory");
     static constexpr int kCodeBytes = 128 * (kUnit / 2);
     static constexpr int kXHalf = PARTS * NT * 128;            // rows of x, 64 k
     static constexpr int kXBytes = 2 * kXHalf;
@@ -59,7 +64,7 @@ struct FewShape {
     // A role that skips units waits by parity, which tells a phase from the one before it
     // only: what it waited for last must lie within the ring.  The copies of x step by four,
     // and a free slot of weights proves that the codes' previous use has landed.
-    static_assert(kStages >= 4 && kStages % 2 == 0 && kSlots <= kStages && kSlots <= kCodeStages, "rings");
+    static_assert(kStages >= 4 && kStages % 2 == 0 && kSlots <= kStages && kSlots <= kCodeStages && kDq <= kSlots, "rings");
     static constexpr int kScaleBytes = 128 * kScaleRow;
     static constexpr int kScaleBufs = 2;
     static constexpr int kBars = 2 * (kCodeStages + kStages + kScaleBufs);
@@ -138,6 +143,8 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
     MoePlan plan = make_plan<1>(g, first_row, first_tile);
     const int half_unit = g.K % kUnit != 0 && g.K % kUnit <= kHalf ? g.K / kUnit : -1;   // the unit of one half
     const int chunk_shift = g.gshift - 3;   // units per chunk of scales: 2^chunk_shift
+    const int set_cols = (PARTS * NT * kUnit) >> g.gshift;                    // columns of a unit's sums
+    const uint32_t sets = min(S::kAccCols / set_cols, S::kStages / 2 * 2);    // 2, 4 or 8 sets, taken in turn
 
     auto fail = [&]() {
         *abort_flag = 1;
@@ -204,8 +211,8 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                     }
                     tc_fence_after();
                     const uint64_t xd = x_desc + static_cast<uint32_t>(r.s) * (S::kXBytes / 16);
-                    const uint32_t a = tmem + S::kAccs * S::kAccCols + (units_issued % S::kSlots) * kSlotCols;
-                    const uint32_t d = tmem + (units_issued % S::kAccs) * S::kAccCols;
+                    const uint32_t a = tmem + S::kAccCols + (units_issued % S::kSlots) * kSlotCols;
+                    const uint32_t d = tmem + (units_issued & (sets - 1)) * set_cols;
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)   // 16 k: 32 bytes of a row of x, 8 columns of weights
@@ -224,8 +231,8 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                 }
             };
             while (ok && next_segment<NT>(plan, s)) {
-                if (S::kPerSet == 1 || g.gshift == 7) segment(std::integral_constant<int, 8>());
-                else if (S::kPerSet == 2 || g.gshift == 6) segment(std::integral_constant<int, 4>());
+                if (S::kMostGroups == 1 || g.gshift == 7) segment(std::integral_constant<int, 8>());
+                else if (S::kMostGroups == 2 || g.gshift == 6) segment(std::integral_constant<int, 4>());
                 else segment(std::integral_constant<int, 2>());
             }
         } else {
@@ -251,7 +258,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
         const int me = (warp - S::kEpiWarp) >> 2;                      // takes units me, me + 2, ...
         const int t = (static_cast<int>(threadIdx.x) - 32 * S::kEpiWarp) & 127;   // lane of tensor memory: weight row
         const int cols = g.swiglu ? g.N >> 1 : g.N;
-        const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + me * S::kAccCols;
+        const uint32_t acc0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         auto sync4 = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };   // the first group
         auto put = [&](Out *p, float v, bool have) {
             if (!have || !ib(p >= static_cast<Out *>(g.y) && p < static_cast<Out *>(g.y) + static_cast<int64_t>(g.R) * cols)) return;
@@ -260,8 +267,9 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
         };
         Ring<S::kStages> r;
         Ring<S::kScaleBufs> rs;
+        for (uint32_t n = me; n < sets; n += S::kEpi)   // the sets of the group's first units are free
+            if (lane == 0) mbar_arrive(ready(n));
         r.step(me);
-        if (lane == 0) mbar_arrive(ready(r.s));   // the set of the group's first unit is free
         uint32_t next = static_cast<uint32_t>(me), before = 0;   // the group's next unit; units of earlier segments
         uint32_t chunk = 0, held = 0;                            // chunks of earlier segments; chunks taken so far
         MoeSegment s;
@@ -292,9 +300,11 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                                    u * GU % kChunk;
                 if (ok && !wait(done(r.s), r.ph)) ok = false;
                 ok = __all_sync(~0u, ok);
+                const int at = r.s;
                 r.step(S::kEpi);
                 if (!ok) continue;
                 tc_fence_after();
+                const uint32_t acc = acc0 + (next & (sets - 1)) * static_cast<uint32_t>(PARTS * NT * GU);
                 if constexpr (GU == 1) {
                     const float w0 = __half2float(sg[0]);
 #pragma unroll
@@ -317,7 +327,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                                 }
                             }
                         }
-                } else if constexpr (GU <= S::kPerSet) {
+                } else if constexpr (GU <= S::kMostGroups) {
                     const bool half = u == half_unit;
 #pragma unroll
                     for (int i = 0; i < GU; i += 2) {   // two groups, their loads in flight together
@@ -353,7 +363,9 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(ready(r.s));   // the set is free for unit next + 2
+                // the set is free for unit next + sets
+                const int later = at + static_cast<int>(sets);
+                if (lane == 0) mbar_arrive(ready(later >= S::kStages ? later - S::kStages : later));
             }
             before += units;
             chunk += static_cast<uint32_t>(((s.k1 - 1) >> (SH - 3)) - first_chunk) + 1;
@@ -370,7 +382,8 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                     const float other = __shfl_xor_sync(~0u, odd ? v[j] : v[j + 1], 1);
                     const float f = scale[j0 + j + odd];
                     const float gate = (odd ? other : v[j]) * f, up = (odd ? v[j + 1] : other) * f;
-                    h[j / 2] = gate / (1.0f + expf(-gate)) * up;
+                    // (bfloat16: the fast exponential and division are off by 2^-20, the rounding by 2^-8)
+                    h[j / 2] = PARTS == 1 ? __fdividef(gate, 1.0f + __expf(-gate)) * up : gate / (1.0f + expf(-gate)) * up;
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -387,6 +400,12 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
         while (next_segment<NT>(plan, s)) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) sum[j] = 0.0f;
+            float f = 0.0f;   // the scale of row t of x, on its way while the sums come in
+            if (me == 0 && t < s.rows) {
+                int src = g.rows != nullptr ? g.rows[s.row0 + t] : s.row0 + t;
+                if (src < 0 || src >= g.Tx) src = g.Tx;
+                f = g.xscale[src];
+            }
             if (g.gshift == 7) drain(std::integral_constant<int, 7>());
             else if (g.gshift == 6) drain(std::integral_constant<int, 6>());
             else drain(std::integral_constant<int, 5>());
@@ -402,15 +421,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
             }
             float *scale = row_scale + buf * NT;
             buf ^= 1;
-            for (int j = t; j < NT; j += 128) {
-                float f = 0.0f;
-                if (j < s.rows) {
-                    int src = g.rows != nullptr ? g.rows[s.row0 + j] : s.row0 + j;
-                    if (src < 0 || src >= g.Tx) src = g.Tx;
-                    f = g.xscale[src];
-                }
-                scale[j] = f;
-            }
+            if (t < NT) scale[t] = f;
             asm volatile("bar.sync 2, 256;" ::: "memory");   // (and makes the row scales visible)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -540,14 +551,14 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
         // ------------------------------------------------------------ dequantisers
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegDq));
         constexpr int G = S::kDq;
-        const int me = (warp - S::kDqWarp) >> 2;   // takes units me, me + 2, ...
+        const int me = (warp - S::kDqWarp) >> 2;   // takes units me, me + kDq, ...
         const int row = (warp & 3) * 32 + lane;    // weight row of the tile = lane of tensor memory
-        const uint32_t slots = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + S::kAccs * S::kAccCols;
+        const uint32_t slots = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + S::kAccCols;
         Ring<S::kCodeStages> rc;
         Ring<S::kStages> rd, r;    // unit next - kSlots, unit next
         Ring<S::kScaleBufs> rs;
         rc.step(me);
-        rd.step(me);
+        rd.step(((me - S::kSlots) % G + G) % G);   // the group's first unit that takes a slot again, less kSlots
         r.step(me);
         uint32_t next = static_cast<uint32_t>(me), before = 0;   // the group's next unit; units of earlier segments
         uint32_t chunk = 0, held = 0;                            // chunks of earlier segments; chunks taken so far
