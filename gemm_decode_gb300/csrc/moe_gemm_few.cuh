@@ -599,17 +599,24 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                 uint4 c4[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) c4[q] = *reinterpret_cast<const uint4 *>(codes + ((q ^ swz) << 4));
+                // 32 codes of one group at a time (beyond K: zero codes, which nothing reads)
+                if (!dq_scales) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {   // 32 codes of one group
-                    if (q >= 2 && u == half_unit) break;
-                    uint32_t z = 8;
-                    if (dq_scales) {
-                        const int grp = ((u * kUnit + q * 32) >> g.gshift) % kChunk;
-                        z = (sz[grp >> 1] >> (4 * (grp & 1))) & 15u;
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t out[16];
+                        decode32<true>(c4[q], 8u, __half2(), out);
+                        tmem_st16(slot + q * 16, out);
                     }
-                    uint32_t out[16];
-                    decode32<true>(c4[q], z, __half2(), out);
-                    tmem_st16(slot + q * 16, out);
+                } else {
+                    // the zero points of the unit's groups: nibbles from the unit's first on
+                    const int g0 = ((u * kUnit) >> g.gshift) % kChunk;
+                    const uint32_t zz = (*reinterpret_cast<const uint16_t *>(sz + (g0 >> 2) * 2)) >> (4 * (g0 & 3));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t out[16];
+                        decode32<true>(c4[q], (zz >> (((q * 32) >> g.gshift) * 4)) & 15u, __half2(), out);
+                        tmem_st16(slot + q * 16, out);
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(code_empty(rc.s));

@@ -499,17 +499,18 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
                 tc_fence_after();
                 const unsigned char *codes = code_ring + rc.s * S::kCodeBytes + t * (128 * kUnit / 2) + row * 64;
                 const unsigned char *sz = scale_ring + rs.s * S::kScaleBytes + (t * 128 + row) * kScaleRow;
-                const bool both = u != half_unit;
                 uint4 c4[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) c4[q] = *reinterpret_cast<const uint4 *>(codes + ((q ^ swz) << 4));
+                // the unit's groups: scales, and zero points as nibbles from the unit's first group on
+                const int g0 = ((u * kUnit) >> g.gshift) % kChunk;
+                const __half *sc = reinterpret_cast<const __half *>(sz) + g0;
+                const uint32_t zz = (*reinterpret_cast<const uint16_t *>(sz + 32 + (g0 >> 2) * 2)) >> (4 * (g0 & 3));
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {   // 32 codes of one group
-                    if (q >= 2 && !both) break;
-                    const int grp = ((u * kUnit + q * 32) >> g.gshift) % kChunk;
-                    const uint32_t z = (sz[32 + (grp >> 1)] >> (4 * (grp & 1))) & 15u;
+                for (int q = 0; q < 4; ++q) {   // 32 codes of one group (beyond K: zero scales)
+                    const int i = (q * 32) >> g.gshift;
                     uint32_t out[16];
-                    decode32<false>(c4[q], z, __half2half2(*reinterpret_cast<const __half *>(sz + 2 * grp)), out);
+                    decode32<false>(c4[q], (zz >> (i * 4)) & 15u, __half2half2(sc[i]), out);
                     tmem_st16(slots + slot * kSlotCols + q * 16, out);
                 }
                 __syncwarp();
