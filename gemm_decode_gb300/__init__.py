@@ -102,6 +102,8 @@ _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 def lib() -> ctypes.CDLL:
     """Load libq4gemv.so (built by gemm_decode_gb300.build); raises if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -185,10 +187,27 @@ def _addr(t, name="argument", esize=0):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """The current torch CUDA stream's address (without building a Stream object where torch
+    offers that: a third of the time)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        try:
+            of, dev = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            of(dev())
+            _raw_stream = lambda: of(dev())  # noqa: E731
+        except (AttributeError, RuntimeError):
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -435,42 +454,54 @@ def vec4_read_probe_run(buf, nbytes, partial, blocks=0, stream=None, check=True)
 
 # ------------------------------------------------------------ mixture of experts
 
+class _Types:
+    """The torch types of the arrays (looked up once)."""
+    f32 = bf16 = i32 = None
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.f32, cls.bf16, cls.i32 = torch.float32, torch.bfloat16, torch.int32
+
+
 def _dtype(t):
     """Q4_F32 or Q4_BF16 of a tensor or a torch dtype (an integer passes through)."""
     if isinstance(t, int):
         return t
-    import torch
+    if _Types.f32 is None:
+        _Types.load()
     d = getattr(t, "dtype", t)
-    if d == torch.float32:
+    if d is _Types.f32:
         return Q4_F32
-    if d == torch.bfloat16:
+    if d is _Types.bf16:
         return Q4_BF16
     raise ValueError(f"float32 or bfloat16 expected, got {d}")
 
 
+def _typed(t, name, dtype):
+    """Address of a contiguous tensor of the given type (None passes through)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is required (got strides {tuple(t.stride())})")
+    return t.data_ptr()
+
+
 def _same(t, name, dtype):
     """Address of an activation array of the call's type (None passes through)."""
-    if t is not None and _dtype(t) != dtype:
-        raise ValueError(f"{name}: has another type than the call's other activations ({t.dtype})")
-    return _addr(t, name)
+    return _typed(t, name, _Types.f32 if dtype == Q4_F32 else _Types.bf16)
 
 
 def _ints(t, name):
     """Address of an int32 array (None passes through)."""
-    if t is not None and not isinstance(t, int):
-        import torch
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name}: int32 expected, got {t.dtype}")
-    return _addr(t, name, 4)
+    return _typed(t, name, _Types.i32)
 
 
 def _floats(t, name):
     """Address of a binary32 array (None passes through)."""
-    if t is not None and not isinstance(t, int):
-        import torch
-        if t.dtype != torch.float32:
-            raise ValueError(f"{name}: float32 expected, got {t.dtype}")
-    return _addr(t, name, 4)
+    return _typed(t, name, _Types.f32)
 
 
 def _need(ok, what):
@@ -505,13 +536,16 @@ def q4moe_route_run(logits, ids, weights, offsets, rows, pos, workspace, bias=No
                     score=Q4_ROUTE_SOFTMAX, renormalize=True, scale=1.0, flags=None, stream=None, check=True) -> int:
     """The top_k experts of each token (ids [T, top_k], weights), and the rows grouped by
     expert (offsets [E + 1], rows [T * top_k], pos [T, top_k])."""
+    if _Types.f32 is None:
+        _Types.load()
     T, E = logits.shape
-    k = ids.shape[1]
-    _need(ids.shape[0] == T and tuple(weights.shape) == (T, k) and tuple(pos.shape) == (T, k) and
-          rows.numel() == T * k and offsets.numel() == E + 1 and (bias is None or bias.numel() == E) and
+    of = ids.shape
+    k = of[1]
+    _need(of[0] == T and weights.shape == of and pos.shape == of and rows.numel() == T * k and
+          offsets.numel() == E + 1 and (bias is None or bias.numel() == E) and
           (token_mask is None or token_mask.numel() == T), "q4moe_route_run: shapes do not agree")
     st = lib().q4moe_route_run(_floats(logits, "logits"), _floats(bias, "bias"), _addr(token_mask, "token_mask", 1),
-                               T, E, k, int(score), 1 if renormalize else 0, float(scale), _ints(ids, "ids"),
+                               T, E, k, score, 1 if renormalize else 0, scale, _ints(ids, "ids"),
                                _floats(weights, "weights"), _ints(offsets, "offsets"), _ints(rows, "rows"),
                                _ints(pos, "pos"), _addr(workspace, "workspace", 1), workspace.numel(),
                                _options(flags, None), _stream(stream))
@@ -528,13 +562,13 @@ def q4moe_gemm_run(codes, scales_f16, zeros_u4_or_null, x, rows, offsets, y, wor
     R = y.shape[0]
     d = _dtype(x)
     _need(K == 2 * half and y.shape[1] == (N // 2 if epilogue == Q4_EPILOGUE_SWIGLU else N) and
-          tuple(scales_f16.shape) == (E, N, K // group) and offsets.numel() == E + 1 and
-          (zeros_u4_or_null is None or tuple(zeros_u4_or_null.shape) == (E, N, (K // group + 1) // 2)) and
+          scales_f16.shape == (E, N, K // group) and offsets.numel() == E + 1 and
+          (zeros_u4_or_null is None or zeros_u4_or_null.shape == (E, N, (K // group + 1) // 2)) and
           (rows is None or rows.numel() == R), "q4moe_gemm_run: shapes do not agree")
     st = lib().q4moe_gemm_run(_addr(codes, "codes", 1), _addr(scales_f16, "scales_f16", 2),
-                              _addr(zeros_u4_or_null, "zeros_u4_or_null", 1), _addr(x, "x"), _ints(rows, "rows"),
-                              _ints(offsets, "offsets"), _same(y, "y", d), E, R, Tx, N, K, int(group), d,
-                              int(epilogue), _addr(workspace, "workspace", 1), workspace.numel(),
+                              _addr(zeros_u4_or_null, "zeros_u4_or_null", 1), _same(x, "x", d), _ints(rows, "rows"),
+                              _ints(offsets, "offsets"), _same(y, "y", d), E, R, Tx, N, K, group, d,
+                              epilogue, _addr(workspace, "workspace", 1), workspace.numel(),
                               _options(flags, wait_timeout_ns), _stream(stream))
     if check:
         _check(st, "q4moe_gemm_run")
@@ -545,7 +579,7 @@ def _gate_stride(gate, T, H):
     if gate is None or gate.dim() == 1:
         _need(gate is None or gate.numel() == H, "gate: [H] or [T, H] expected")
         return 0
-    _need(tuple(gate.shape) == (T, H), "gate: [H] or [T, H] expected")
+    _need(gate.shape == (T, H), "gate: [H] or [T, H] expected")
     return H
 
 
@@ -556,14 +590,14 @@ def q4_block_norm_run(y, x, out, pos=None, weights=None, post_gamma=None, gate=N
     T, H = x.shape
     k = pos.shape[1] if pos is not None else 0
     d = _dtype(x)
-    _need(y.shape[1] == H and tuple(out.shape) == (T, H) and (out_norm is None or tuple(out_norm.shape) == (T, H)) and
-          (pos is None or (pos.shape[0] == T and weights is not None and tuple(weights.shape) == (T, k))) and
+    _need(y.shape[1] == H and out.shape == x.shape and (out_norm is None or out_norm.shape == x.shape) and
+          (pos is None or (pos.shape[0] == T and weights is not None and weights.shape == pos.shape)) and
           (post_gamma is None or post_gamma.numel() == H) and (pre_gamma is None or pre_gamma.numel() == H),
           "q4_block_norm_run: shapes do not agree")
     a = _BlockNorm(T, H, k, d, y.shape[0], _same(y, "y", d), _ints(pos, "pos"), _floats(weights, "weights"),
-                   _addr(x, "x"), _floats(post_gamma, "post_gamma"), _same(gate, "gate", d),
+                   _same(x, "x", d), _floats(post_gamma, "post_gamma"), _same(gate, "gate", d),
                    _gate_stride(gate, T, H), _floats(pre_gamma, "pre_gamma"), _same(out, "out", d),
-                   _same(out_norm, "out_norm", d), float(residual_scale), float(eps))
+                   _same(out_norm, "out_norm", d), residual_scale, eps)
     st = lib().q4_block_norm_run(ctypes.byref(a), _options(flags, None), _stream(stream))
     if check:
         _check(st, "q4_block_norm_run")
@@ -582,19 +616,19 @@ def q4moe_block_run(up, down, logits, a, x, out, out_norm, ids, route_weights, w
     k = ids.shape[1]
     d = _dtype(x)
     for (codes, scales, zeros), N, K in ((up, 2 * inner, H), (down, H, inner)):
-        _need(tuple(codes.shape) == (E, N, K // 2) and tuple(scales.shape) == (E, N, K // group) and
-              (zeros is None or tuple(zeros.shape) == (E, N, (K // group + 1) // 2)),
+        _need(codes.shape == (E, N, K // 2) and scales.shape == (E, N, K // group) and
+              (zeros is None or zeros.shape == (E, N, (K // group + 1) // 2)),
               "q4moe_block_run: shapes of the weights do not agree")
-    _need(x.shape[0] == T and tuple(a.shape) == (T, H) and tuple(out.shape) == (T, H) and
-          (out_norm is None or tuple(out_norm.shape) == (T, H)) and tuple(ids.shape) == (T, k) and
-          tuple(route_weights.shape) == (T, k) and (bias is None or bias.numel() == E) and
+    _need(x.shape[0] == T and a.shape == x.shape and out.shape == x.shape and
+          (out_norm is None or out_norm.shape == x.shape) and ids.shape == (T, k) and
+          route_weights.shape == (T, k) and (bias is None or bias.numel() == E) and
           (token_mask is None or token_mask.numel() == T) and (post_gamma is None or post_gamma.numel() == H) and
           (pre_gamma is None or pre_gamma.numel() == H), "q4moe_block_run: shapes do not agree")
-    g = _MoeBlock(T, E, k, H, inner, int(group), d, int(score), 1 if renormalize else 0, float(route_scale),
-                  float(residual_scale), float(eps), _addr(up[0], "up codes", 1), _addr(up[1], "up scales", 2),
+    g = _MoeBlock(T, E, k, H, inner, group, d, score, 1 if renormalize else 0, route_scale,
+                  residual_scale, eps, _addr(up[0], "up codes", 1), _addr(up[1], "up scales", 2),
                   _addr(up[2], "up zeros", 1), _addr(down[0], "down codes", 1), _addr(down[1], "down scales", 2),
                   _addr(down[2], "down zeros", 1), _floats(logits, "logits"), _floats(bias, "bias"),
-                  _addr(token_mask, "token_mask", 1), _same(a, "a", d), _addr(x, "x"),
+                  _addr(token_mask, "token_mask", 1), _same(a, "a", d), _same(x, "x", d),
                   _floats(post_gamma, "post_gamma"), _same(gate, "gate", d), _gate_stride(gate, T, H),
                   _floats(pre_gamma, "pre_gamma"), _ints(ids, "ids"), _floats(route_weights, "route_weights"),
                   _same(out, "out", d), _same(out_norm, "out_norm", d), _addr(workspace, "workspace", 1),

@@ -8,8 +8,10 @@
 // One CTA per token; each thread keeps its NI vectors of the row in registers from the
 // first load to the last store, so every array is read or written once and the two means
 // are block sums of registers (binary32, in a fixed order: warps by shuffles, then the
-// warps' sums by every thread).  Loads are 16 bytes per thread (8 bf16 or 4 floats); rows
-// whose length is no multiple of that, or whose gate is unaligned, take single elements.
+// warps' sums by every thread).  Loads are up to 16 bytes per thread, four of
+// the token's rows of y at a time in flight together, and those of x and the gate before
+// them, so that no load waits for a sum; rows whose length is no multiple of 16 bytes, or
+// whose gate or norm weights are unaligned, take accesses of 8, 4 or 2 bytes.
 //
 // Bound: the bytes of the rows of y, x and the outputs for prompts; latency for decoding.
 #include <cuda_bf16.h>
@@ -31,17 +33,31 @@ __device__ __forceinline__ T from_float(float v) {
     else return v;
 }
 
-// V consecutive elements in one access (V * sizeof(T) is 16 bytes, or V is 1).
+// V consecutive elements in one access of up to 16 bytes.
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Pack {
     T v[V];
 };
 
 template <typename T, int V>
-__device__ __forceinline__ void load_pack(const T *p, float *out) {
-    const Pack<T, V> a = *reinterpret_cast<const Pack<T, V> *>(p);
+__device__ __forceinline__ Pack<T, V> load_pack(const T *p) {
+    return *reinterpret_cast<const Pack<T, V> *>(p);
+}
+// V consecutive norm weights (aligned to the smaller of 4 V and 16 bytes).
+template <int V>
+__device__ __forceinline__ void load_floats(const float *p, float *out) {
+    if constexpr (V == 1) {
+        out[0] = *p;
+    } else if constexpr (V == 2) {
+        const float2 a = *reinterpret_cast<const float2 *>(p);
+        out[0] = a.x, out[1] = a.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = to_float(a.v[i]);
+        for (int i = 0; i < V; i += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(p + i);
+            out[i] = a.x, out[i + 1] = a.y, out[i + 2] = a.z, out[i + 3] = a.w;
+        }
+    }
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_pack(T *p, const float *in) {
@@ -81,24 +97,54 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const q4_block_norm_t 
         pos_s[threadIdx.x] = p >= 0 && p < g.R ? p : -1;
         w_s[threadIdx.x] = g.weights[at];
     }
+    // the residual and the gate are on their way while the rows of y are summed
+    Pack<T, V> xv[NI], gv[NI];
     float b[NI][V];
+    const T *gate = g.gate != nullptr ? static_cast<const T *>(g.gate) + static_cast<int64_t>(t) * g.gate_stride : nullptr;
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+    for (int i = 0; i < NI; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * V;
+        if (c < H) {
+            xv[i] = load_pack<T, V>(x + c);
+            if (gate != nullptr) gv[i] = load_pack<T, V>(gate + c);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) b[i][v] = 0.0f;
-    if (g.top_k > 0) __syncthreads();
-    for (int j = 0; j < (g.top_k > 0 ? g.top_k : 1); ++j) {
-        const int64_t row = g.top_k > 0 ? pos_s[j] : t;
-        if (row < 0) continue;
-        const float w = g.top_k > 0 ? w_s[j] : 1.0f;
+    }
+    if (g.top_k > 0) {
+        __syncthreads();
+        for (int j0 = 0; j0 < g.top_k; j0 += 4) {
+            const T *row[4];
+            float w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int p = j0 + q < g.top_k ? pos_s[j0 + q] : -1;
+                row[q] = p >= 0 ? y + static_cast<int64_t>(p) * H : nullptr;
+                w[q] = p >= 0 ? w_s[j0 + q] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int c = (i * blockDim.x + threadIdx.x) * V;
+                if (c < H) {
+                    Pack<T, V> in[4] = {};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (row[q] != nullptr) in[q] = load_pack<T, V>(row[q] + c);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int v = 0; v < V; ++v) b[i][v] = fmaf(w[q], to_float(in[q].v[v]), b[i][v]);
+                }
+            }
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * V;
             if (c < H) {
-                float in[V];
-                load_pack<T, V>(y + row * H + c, in);
+                const Pack<T, V> in = load_pack<T, V>(y + static_cast<int64_t>(t) * H + c);
 #pragma unroll
-                for (int v = 0; v < V; ++v) b[i][v] = fmaf(w, in[v], b[i][v]);
+                for (int v = 0; v < V; ++v) b[i][v] = to_float(in.v[v]);
             }
         }
     }
@@ -113,8 +159,10 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const q4_block_norm_t 
         for (int i = 0; i < NI; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * V;
             if (c < H) {
+                float w[V];
+                load_floats<V>(g.post_gamma + c, w);
 #pragma unroll
-                for (int v = 0; v < V; ++v) b[i][v] = b[i][v] * r * g.post_gamma[c + v];
+                for (int v = 0; v < V; ++v) b[i][v] = b[i][v] * r * w[v];
             }
         }
     }
@@ -123,16 +171,10 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const q4_block_norm_t 
     for (int i = 0; i < NI; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
         if (c < H) {
-            float in[V];
-            if (g.gate != nullptr) {
-                load_pack<T, V>(static_cast<const T *>(g.gate) + static_cast<int64_t>(t) * g.gate_stride + c, in);
-#pragma unroll
-                for (int v = 0; v < V; ++v) b[i][v] *= in[v];
-            }
-            load_pack<T, V>(x + c, in);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                b[i][v] = fmaf(g.residual_scale, in[v], b[i][v]);
+                if (gate != nullptr) b[i][v] *= to_float(gv[i].v[v]);
+                b[i][v] = fmaf(g.residual_scale, to_float(xv[i].v[v]), b[i][v]);
                 ss = fmaf(b[i][v], b[i][v], ss);
             }
             store_pack<T, V>(static_cast<T *>(g.out) + static_cast<int64_t>(t) * H + c, b[i]);
@@ -144,8 +186,10 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const q4_block_norm_t 
     for (int i = 0; i < NI; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
         if (c < H) {
+            float w[V];
+            load_floats<V>(g.pre_gamma + c, w);
 #pragma unroll
-            for (int v = 0; v < V; ++v) b[i][v] = b[i][v] * r * g.pre_gamma[c + v];
+            for (int v = 0; v < V; ++v) b[i][v] = b[i][v] * r * w[v];
             store_pack<T, V>(static_cast<T *>(g.out_norm) + static_cast<int64_t>(t) * H + c, b[i]);
         }
     }
@@ -154,20 +198,35 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const q4_block_norm_t 
 template <typename T, int V>
 static int launch_norm(const q4_block_norm_t &a, cudaStream_t stream) {
     const bool overlap = call_options().overlap;
-    const int vecs = (a.H + V - 1) / V;
-    auto threads = [&](int ni) { return dim3(static_cast<unsigned>((((vecs + ni - 1) / ni) + 31) / 32 * 32)); };
-    const dim3 grid(static_cast<unsigned>(a.T));
-    if (vecs <= 1024) return launch_overlappable(block_norm_kernel<T, V, 1>, grid, threads(1), 0, stream, overlap, a);
-    if (vecs <= 4096) return launch_overlappable(block_norm_kernel<T, V, 4>, grid, threads(4), 0, stream, overlap, a);
-    return launch_overlappable(block_norm_kernel<T, V, 16>, grid, threads(16), 0, stream, overlap, a);
+    const int vecs = a.H / V;
+    auto launch = [&](auto kernel, int ni) {
+        const unsigned threads = static_cast<unsigned>(((vecs + ni - 1) / ni + 31) / 32 * 32);
+        return launch_overlappable(kernel, dim3(static_cast<unsigned>(a.T)), dim3(threads), 0, stream, overlap, a);
+    };
+    // vectors per thread: H is at most 16384
+    constexpr int kMost = kMaxNormH / V / 1024;
+    if (vecs <= 1024) return launch(block_norm_kernel<T, V, 1>, 1);
+    if constexpr (kMost > 2)
+        if (vecs > 2048) return launch(block_norm_kernel<T, V, kMost>, kMost);
+    return launch(block_norm_kernel<T, V, 2>, 2);
+}
+
+// The widest access that the row's length and the alignment of the gate and of the norm
+// weights allow.
+template <typename T>
+static int launch_norm_of(const q4_block_norm_t &a, cudaStream_t stream) {
+    auto fits = [&](int v) {
+        const uintptr_t w = v >= 4 ? 16 : 4 * v;
+        return a.H % v == 0 && aligned(a.gate, v * sizeof(T)) && aligned(a.post_gamma, w) && aligned(a.pre_gamma, w);
+    };
+    if constexpr (sizeof(T) == 2)
+        if (fits(8)) return launch_norm<T, 8>(a, stream);
+    if (fits(4)) return launch_norm<T, 4>(a, stream);
+    return fits(2) ? launch_norm<T, 2>(a, stream) : launch_norm<T, 1>(a, stream);
 }
 
 int launch_block_norm(const q4_block_norm_t &a, cudaStream_t stream) {
-    if (a.dtype == Q4_F32)
-        return a.H % 4 == 0 && aligned(a.gate, 16) ? launch_norm<float, 4>(a, stream)
-                                                   : launch_norm<float, 1>(a, stream);
-    return a.H % 8 == 0 && aligned(a.gate, 16) ? launch_norm<__nv_bfloat16, 8>(a, stream)
-                                               : launch_norm<__nv_bfloat16, 1>(a, stream);
+    return a.dtype == Q4_F32 ? launch_norm_of<float>(a, stream) : launch_norm_of<__nv_bfloat16>(a, stream);
 }
 
 }  // namespace q4
