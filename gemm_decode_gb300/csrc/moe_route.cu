@@ -8,9 +8,9 @@
 // rounded scores: softmax and sigmoid rise with the logit, so the choice never needs them.
 //
 // The grouped order is a counting sort that keeps the order of the tokens.  A block of
-// 1024 choices counts them per warp with one match over the warp (the rank inside the
+// 512 choices counts them per warp with one match over the warp (the rank inside the
 // warp is the number of earlier lanes of the match), then sums the counts of the warps
-// before.  With one block (up to 1024 choices: all of decoding) the same launch adds the
+// before.  With one block (up to 512 choices: decoding) the same launch adds the
 // prefix over the experts and is done; with more, each block writes its histogram and a
 // second launch adds the histograms of the blocks before it.  No atomics: the order is
 // the same on every run.
@@ -23,7 +23,7 @@ namespace q4 {
 
 namespace {
 
-constexpr int kChoices = 1024;   // choices (token, place) ranked by one block
+constexpr int kChoices = 512;   // choices (token, place) ranked by one block
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -75,7 +75,7 @@ __device__ __forceinline__ int block_prefix(int v, int *sums, int *total) {
 
 // One block: the choices of tokens [blockIdx.x * per_block, ...).  NV: logits per lane.
 template <int NV>
-__global__ void __launch_bounds__(1024) route_choose_kernel(const RouteArgs a, int per_block, int single) {
+__global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteArgs a, int per_block, int single) {
     extern __shared__ unsigned char route_smem[];
     int *chosen = reinterpret_cast<int *>(route_smem);                     // [kChoices]
     int *base = chosen + kChoices;                                         // [E] first row of an expert (single)
@@ -89,21 +89,29 @@ __global__ void __launch_bounds__(1024) route_choose_kernel(const RouteArgs a, i
     for (int i = threadIdx.x; i < warps * a.E; i += blockDim.x) count[i] = 0;
     wait_prior_grid();
     allow_next_grid();
+    // the logits of the warp's next token are on their way while this one's are ranked
+    float ahead[NV];
+    bool ahead_live = false;
+    auto fetch = [&](int i) {
+        if (i >= tokens) return;
+        const int t = t0 + i;
+        ahead_live = a.mask == nullptr || a.mask[t] != 0;
+        const float *l = a.logits + static_cast<int64_t>(t) * a.E;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) ahead[c] = c * 32 + lane < a.E ? l[c * 32 + lane] : -INFINITY;
+    };
+    fetch(warp);
     for (int i = warp; i < tokens; i += warps) {
         const int t = t0 + i;
         const int64_t at = static_cast<int64_t>(t) * a.k;
-        const bool live = a.mask == nullptr || a.mask[t] != 0;
+        const bool live = ahead_live;
+        float v[NV];
+#pragma unroll
+        for (int c = 0; c < NV; ++c) v[c] = ahead[c] == ahead[c] ? ahead[c] : -INFINITY;   // NaN counts as -inf
+        fetch(i + warps);
         int mine = -1;   // lane j: the token's j-th choice
         float m_all = -INFINITY, s_all = 0.0f;
         if (live) {
-            const float *l = a.logits + static_cast<int64_t>(t) * a.E;
-            float v[NV];
-#pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                const int e = c * 32 + lane;
-                v[c] = e < a.E ? l[e] : -INFINITY;
-                if (!(v[c] == v[c])) v[c] = -INFINITY;   // NaN counts as -inf
-            }
             if (!a.sigmoid && !a.renorm) {
 #pragma unroll
                 for (int c = 0; c < NV; ++c) m_all = fmaxf(m_all, v[c]);
@@ -261,7 +269,7 @@ int launch_route(const RouteArgs &a, cudaStream_t stream) {
     const int per = route_per_block(a.k);
     const int blocks = (a.T + per - 1) / per;
     // a thread per choice and per expert of the block
-    const int need = blocks > 1 ? kChoices : (a.T * a.k > a.E ? a.T * a.k : a.E);
+    const int choices = blocks > 1 ? kChoices : a.T * a.k, need = choices > a.E ? choices : a.E;
     const int threads = need <= 128 ? 128 : (need + 31) / 32 * 32;
     int st;
     if (a.E <= 32) st = launch_choose<1>(a, blocks, threads, per, stream);
