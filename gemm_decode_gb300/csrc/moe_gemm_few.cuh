@@ -16,10 +16,9 @@
 //                MMA took 107 cycles; this way 24, and 16 is what the tensor core needs for
 //                up to 32 columns), then one commit
 //   warps 2, 3   scales and zero points, 16 groups per row at a time
-//   warps 4-11   epilogue, two groups of four warps taking the units in turn: sums of the
-//                unit's groups from tensor memory into registers; at the end of an item the
-//                second hands its sums to the first, which scales, applies SwiGLU, rounds
-//                and stores
+//   warps 4-11   epilogue, two groups of four warps taking the items in turn: the sums of each
+//                unit's groups from tensor memory into registers; at the end of an item scale,
+//                SwiGLU, rounding and store, while the other group takes the next item's sums
 //   warps 12-15  copy the rows of x, by index, one unit each in turn (16-byte asynchronous
 //                copies: a bulk copy of four rows by index took a lane 80 to 140 cycles)
 //   the rest     dequantisers, three groups (two with 64 rows of x) of four warps taking the units in turn: a thread
@@ -66,12 +65,11 @@ struct FewShape {
     // and a free slot of weights proves that the codes' previous use has landed.
     static_assert(kStages >= 4 && kStages % 2 == 0 && kSlots <= kStages && kSlots <= kCodeStages && kDq <= kSlots, "rings");
     static constexpr int kScaleBytes = 128 * kScaleRow;
-    static constexpr int kScaleBufs = 2;
+    static constexpr int kScaleBufs = 4;
     static constexpr int kBars = 2 * (kCodeStages + kStages + kScaleBufs);
     static constexpr size_t fixed() {
         return 1024 + static_cast<size_t>(kStages) * kXBytes + static_cast<size_t>(kCodeStages) * kCodeBytes +
-               static_cast<size_t>(kScaleBufs) * kScaleBytes + static_cast<size_t>(NT) * 128 * 4 + 8 * kBars +
-               2 * NT * 4 + 4 * NT * 4 + 64;
+               static_cast<size_t>(kScaleBufs) * kScaleBytes + 8 * kBars + 2 * kEpi * NT * 4 + 4 * NT * 4 + 64;
     }
     static constexpr size_t smem(int E) { return fixed() + 8 * (static_cast<size_t>(E) + 1); }
 };
@@ -88,13 +86,12 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
     unsigned char *x_ring = smem;
     unsigned char *code_ring = x_ring + S::kStages * S::kXBytes;
     unsigned char *scale_ring = code_ring + S::kCodeStages * S::kCodeBytes;
-    float *handed = reinterpret_cast<float *>(scale_ring + S::kScaleBufs * S::kScaleBytes);   // [NT][128]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(handed + NT * 128);
-    float *row_scale = reinterpret_cast<float *>(bars + S::kBars);   // [2][NT]
-    int *x_rows = reinterpret_cast<int *>(row_scale + 2 * NT);       // [4][NT] rows of x, a list per copying warp
+    uint64_t *bars = reinterpret_cast<uint64_t *>(scale_ring + S::kScaleBufs * S::kScaleBytes);
+    float *row_scale = reinterpret_cast<float *>(bars + S::kBars);   // [epilogue group][2][NT]
+    int *x_rows = reinterpret_cast<int *>(row_scale + 2 * S::kEpi * NT);   // [4][NT] rows of x, a list per copying warp
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(x_rows + 4 * NT);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *last_flag = reinterpret_cast<int *>(tmem_slot + 2);
+    int *last_flag = reinterpret_cast<int *>(tmem_slot + 2);         // [epilogue group]
     int *first_row = reinterpret_cast<int *>(tmem_slot + 4);         // [E + 1]
     int *first_tile = first_row + g.E + 1;                           // [E + 1]
 
@@ -123,7 +120,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
         }
         for (int s = 0; s < S::kScaleBufs; ++s) {
             mbar_init(sc_full(s), 2);
-            mbar_init(sc_empty(s), 4 * S::kEpi + (dq_scales ? 4 * S::kDq : 0));
+            mbar_init(sc_empty(s), 4 + (dq_scales ? 4 * S::kDq : 0));   // one epilogue group, all dequantisers
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -255,120 +252,105 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
     } else if (warp < S::kXWarp) {
         // ------------------------------------------------------------ epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegSums));
-        const int me = (warp - S::kEpiWarp) >> 2;                      // takes units me, me + 2, ...
+        const int me = (warp - S::kEpiWarp) >> 2;                      // takes segments me, me + 2, ...
         const int t = (static_cast<int>(threadIdx.x) - 32 * S::kEpiWarp) & 127;   // lane of tensor memory: weight row
         const int cols = g.swiglu ? g.N >> 1 : g.N;
         const uint32_t acc0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        auto sync4 = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };   // the first group
+        auto sync4 = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + me) : "memory"); };
         auto put = [&](Out *p, float v, bool have) {
             if (!have || !ib(p >= static_cast<Out *>(g.y) && p < static_cast<Out *>(g.y) + static_cast<int64_t>(g.R) * cols)) return;
             if constexpr (PARTS == 1) *p = __float2bfloat16_rn(v);
             else *p = v;
         };
-        Ring<S::kStages> r;
-        Ring<S::kScaleBufs> rs;
-        for (uint32_t n = me; n < sets; n += S::kEpi)   // the sets of the group's first units are free
-            if (lane == 0) mbar_arrive(ready(n));
-        r.step(me);
-        uint32_t next = static_cast<uint32_t>(me), before = 0;   // the group's next unit; units of earlier segments
-        uint32_t chunk = 0, held = 0;                            // chunks of earlier segments; chunks taken so far
+        if (me == 0)
+            for (uint32_t n = 0; n < sets; ++n)   // every set is free
+                if (lane == 0) mbar_arrive(ready(n));
+        uint32_t before = 0, chunk = 0;   // units and chunks of earlier segments
         MoeSegment s;
         int buf = 0;
-        bool ok = true, handing = false;
+        bool ok = true;
         float sum[NT];
-        auto take_chunk = [&]() {   // let go of the chunk held and wait for the next
-            if (held > 0) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sc_empty(rs.s));
-                rs.step();
-            }
-            ++held;
-            if (ok && !wait(sc_full(rs.s), rs.ph)) ok = false;
-            ok = __all_sync(~0u, ok);
-        };
-        // the group's units of the segment, for groups of 2^SH weights: straight-line code per unit
-        auto drain = [&](auto shift) {
-            constexpr int SH = decltype(shift)::value, GU = kUnit >> SH;   // groups in a unit
-            const uint32_t units = static_cast<uint32_t>(s.k1 - s.k0);
+        // The segment's units, kMostGroups groups of weights at a time: one wait and one round
+        // of arrivals for up to four units (one at a time, a unit took 940 cycles).
+        auto drain = [&]() {
+            constexpr int MG = S::kMostGroups;
+            const int lg = 7 - g.gshift;                      // a unit has 2^lg groups
             const int n16 = (s.rows + 15) & ~15;
-            const int first_chunk = s.k0 >> (SH - 3);
-            for (; next - before < units; next += S::kEpi) {
-                const int u = s.k0 + static_cast<int>(next - before);
-                const uint32_t want = chunk + static_cast<uint32_t>((u >> (SH - 3)) - first_chunk) + 1;
-                while (held < want) take_chunk();
-                const __half *sg = reinterpret_cast<const __half *>(scale_ring + rs.s * S::kScaleBytes + t * kScaleRow) +
-                                   u * GU % kChunk;
-                if (ok && !wait(done(r.s), r.ph)) ok = false;
+            const int chunk0 = s.k0 >> chunk_shift, in_chunk = (1 << chunk_shift) - 1;
+            uint32_t unit = before;
+            const __half *sc = nullptr;
+            for (int u = s.k0; u < s.k1;) {
+                const uint32_t c = chunk + static_cast<uint32_t>((u >> chunk_shift) - chunk0);
+                if (u == s.k0 || (u & in_chunk) == 0) {   // the next chunk of scales
+                    if (ok && !wait(sc_full(c % S::kScaleBufs), c / S::kScaleBufs & 1u)) ok = false;
+                    sc = reinterpret_cast<const __half *>(scale_ring + c % S::kScaleBufs * S::kScaleBytes + t * kScaleRow);
+                }
+                const int units = min(min(MG >> lg, s.k1 - u), in_chunk + 1 - (u & in_chunk));
+                const bool half = u + units - 1 == half_unit;
+                const int groups = (units << lg) - (half ? 1 << lg >> 1 : 0);
+                const uint32_t last = unit + units - 1;
+                if (ok && !wait(done(last % S::kStages), last / S::kStages & 1u)) ok = false;
                 ok = __all_sync(~0u, ok);
-                const int at = r.s;
-                r.step(S::kEpi);
-                if (!ok) continue;
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = acc0 + (next & (sets - 1)) * static_cast<uint32_t>(PARTS * NT * GU);
-                if constexpr (GU == 1) {
+                const __half *sg = sc + ((u << lg) & (kChunk - 1));
+                auto at = [&](int i) {   // the sums of group i
+                    return acc0 + ((unit + (i >> lg)) & (sets - 1)) * static_cast<uint32_t>(set_cols) +
+                           (i & ((1 << lg) - 1)) * (PARTS * NT);
+                };
+                if constexpr (MG == 1) {
                     const float w0 = __half2float(sg[0]);
 #pragma unroll
                     for (int j0 = 0; j0 < NT; j0 += 16)
                         if (j0 < s.rows) {
                             float v[16];
-                            if constexpr (PARTS == 2 && NT <= 32) {
-                                float c[16];   // from the second part of x
-                                tmem_ld16x2(acc + j0, acc + n16 + j0, v, c);
+                            tmem_ld16(at(0) + j0, v);
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) sum[j0 + j] = fmaf(w0, v[j] + c[j], sum[j0 + j]);
-                            } else {
-                                tmem_ld16(acc + j0, v);
+                            for (int j = 0; j < 16; ++j) sum[j0 + j] = fmaf(w0, v[j], sum[j0 + j]);
+                            if constexpr (PARTS == 2) {   // from the second part of x
+                                tmem_ld16(at(0) + n16 + j0, v);
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) sum[j0 + j] = fmaf(w0, v[j], sum[j0 + j]);
-                                if constexpr (PARTS == 2) {
-                                    tmem_ld16(acc + n16 + j0, v);
-#pragma unroll
-                                    for (int j = 0; j < 16; ++j) sum[j0 + j] = fmaf(w0, v[j], sum[j0 + j]);
-                                }
                             }
                         }
-                } else if constexpr (GU <= S::kMostGroups) {
-                    const bool half = u == half_unit;
+                } else {
 #pragma unroll
-                    for (int i = 0; i < GU; i += 2) {   // two groups, their loads in flight together
-                        if (half && i * 2 >= GU && i > 0) break;   // the second half of the unit
-                        const uint32_t a0 = acc + i * (PARTS * NT), a1 = a0 + PARTS * NT;
-                        const float w0 = __half2float(sg[i]);
-                        // half of a unit of two groups: there is no second group, and its sums are stale
-                        const bool two = GU > 2 || !half;
-                        const float w1 = two ? __half2float(sg[i + 1]) : 0.0f;
-                        if constexpr (PARTS == 1) {
+                    for (int i = 0; i < MG; i += 2)   // two groups, their loads in flight together
+                        if (i < groups) {
+                            const bool two = i + 1 < groups;
+                            const uint32_t a0 = at(i), a1 = two ? at(i + 1) : a0;
+                            const float w0 = __half2float(sg[i]), w1 = two ? __half2float(sg[i + 1]) : 0.0f;
+                            if constexpr (PARTS == 1) {
 #pragma unroll
-                            for (int j0 = 0; j0 < NT; j0 += 16)
-                                if (j0 < s.rows) {
-                                    float v0[16], v1[16];
-                                    tmem_ld16x2(a0 + j0, a1 + j0, v0, v1);
+                                for (int j0 = 0; j0 < NT; j0 += 16)
+                                    if (j0 < s.rows) {
+                                        float v0[16], v1[16];
+                                        tmem_ld16x2(a0 + j0, a1 + j0, v0, v1);
 #pragma unroll
-                                    for (int j = 0; j < 16; ++j)
-                                        sum[j0 + j] = fmaf(w1, two ? v1[j] : 0.0f, fmaf(w0, v0[j], sum[j0 + j]));
-                                }
-                        } else {
+                                        for (int j = 0; j < 16; ++j)
+                                            sum[j0 + j] = fmaf(w1, v1[j], fmaf(w0, v0[j], sum[j0 + j]));
+                                    }
+                            } else {
 #pragma unroll
-                            for (int j0 = 0; j0 < NT; j0 += 8)
-                                if (j0 < s.rows) {
-                                    float v0[8], c0[8], v1[8], c1[8];
-                                    tmem_ld8x4(a0 + j0, a0 + n16 + j0, a1 + j0, a1 + n16 + j0, v0, c0, v1, c1);
+                                for (int j0 = 0; j0 < NT; j0 += 8)
+                                    if (j0 < s.rows) {
+                                        float v0[8], c0[8], v1[8], c1[8];
+                                        tmem_ld8x4(a0 + j0, a0 + n16 + j0, a1 + j0, a1 + n16 + j0, v0, c0, v1, c1);
 #pragma unroll
-                                    for (int j = 0; j < 8; ++j)
-                                        sum[j0 + j] = fmaf(w1, two ? v1[j] + c1[j] : 0.0f,
-                                                           fmaf(w0, v0[j] + c0[j], sum[j0 + j]));
-                                }
+                                        for (int j = 0; j < 8; ++j)
+                                            sum[j0 + j] = fmaf(w1, v1[j] + c1[j], fmaf(w0, v0[j] + c0[j], sum[j0 + j]));
+                                    }
+                            }
                         }
-                    }
                 }
                 tc_fence_before();
                 __syncwarp();
-                // the set is free for unit next + sets
-                const int later = at + static_cast<int>(sets);
-                if (lane == 0) mbar_arrive(ready(later >= S::kStages ? later - S::kStages : later));
+                // each set is free for the unit that comes `sets` later
+                if (lane < units) mbar_arrive(ready(static_cast<int>((unit + lane + sets) % S::kStages)));
+                unit += units;
+                u += units;
+                if (lane == 0 && (u == s.k1 || (u & in_chunk) == 0)) mbar_arrive(sc_empty(c % S::kScaleBufs));
             }
-            before += units;
-            chunk += static_cast<uint32_t>(((s.k1 - 1) >> (SH - 3)) - first_chunk) + 1;
         };
         // 16 columns (rows of x from j0 on) of weight row n, unscaled sums in v
         auto finish = [&](int n, int j0, const float *v, const float *scale) {
@@ -397,36 +379,34 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
         };
         // After a failed wait the groups go on through the barriers they share, without
         // waiting for anything else and without storing.
-        while (next_segment<NT>(plan, s)) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) sum[j] = 0.0f;
-            float f = 0.0f;   // the scale of row t of x, on its way while the sums come in
-            if (me == 0 && t < s.rows) {
-                int src = g.rows != nullptr ? g.rows[s.row0 + t] : s.row0 + t;
-                if (src < 0 || src >= g.Tx) src = g.Tx;
-                f = g.xscale[src];
-            }
-            if (g.gshift == 7) drain(std::integral_constant<int, 7>());
-            else if (g.gshift == 6) drain(std::integral_constant<int, 6>());
-            else drain(std::integral_constant<int, 5>());
-            if (me == 1) {
-                // the second group's sums go to the first
-                if (handing) asm volatile("bar.sync 3, 256;" ::: "memory");   // the last ones have been read
-                handing = true;
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    if (j < s.rows) handed[j * 128 + t] = sum[j];
-                asm volatile("bar.sync 2, 256;" ::: "memory");
+        for (int turn = 0; next_segment<NT>(plan, s); turn ^= 1) {
+            const uint32_t units = static_cast<uint32_t>(s.k1 - s.k0);
+            const uint32_t chunks = static_cast<uint32_t>(((s.k1 - 1) >> chunk_shift) - (s.k0 >> chunk_shift)) + 1;
+            if (turn != me) {
+                before += units;
+                chunk += chunks;
                 continue;
             }
-            float *scale = row_scale + buf * NT;
-            buf ^= 1;
-            if (t < NT) scale[t] = f;
-            asm volatile("bar.sync 2, 256;" ::: "memory");   // (and makes the row scales visible)
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if (j < s.rows) sum[j] += handed[j * 128 + t];
-            asm volatile("bar.arrive 3, 256;" ::: "memory");   // (read: the second group may write again)
+            for (int j = 0; j < NT; ++j) sum[j] = 0.0f;
+            float *scale = row_scale + (2 * me + buf) * NT;
+            buf ^= 1;
+            if (t < NT) {
+                float f = 0.0f;
+                if (t < s.rows) {
+                    int src = g.rows != nullptr ? g.rows[s.row0 + t] : s.row0 + t;
+                    if (src < 0 || src >= g.Tx) src = g.Tx;
+                    f = g.xscale[src];
+                }
+                scale[t] = f;
+            }
+            // the other group has taken the sums of the segment before (barriers 3, 4)
+            if (before > 0) asm volatile("bar.sync %0, 256;" ::"r"(3 + me) : "memory");
+            sync4();   // the row scales are there
+            drain();
+            before += units;
+            chunk += chunks;
+            if (plan.at < plan.end) asm volatile("bar.arrive %0, 256;" ::"r"(4 - me) : "memory");
             const int n = s.group * 128 + t;
             if (s.k1 - s.k0 == static_cast<int>(plan.units)) {
                 if (ok)
@@ -447,9 +427,9 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                 if (j < s.rows) mine[j * 128] = sum[j];
             __threadfence();
             sync4();
-            if (t == 0) *last_flag = atomicAdd(g.arrived + c0, 1u) == c1 - c0;
+            if (t == 0) last_flag[me] = atomicAdd(g.arrived + c0, 1u) == c1 - c0;
             sync4();
-            if (*last_flag != 0 && ok) {
+            if (last_flag[me] != 0 && ok) {
                 __threadfence();
 #pragma unroll 1
                 for (int j0 = 0; j0 < s.rows; j0 += 16) {
@@ -467,8 +447,6 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
             }
             sync4();   // last_flag is read before the next item's
         }
-        if (me == 1 && handing) asm volatile("bar.sync 3, 256;" ::: "memory");
-        while (ok && held < chunk) take_chunk();   // the other readers need the chunks after this group's last
     } else if (warp < S::kDqWarp) {
         // ------------------------------------------------------------ rows of x
         // The four warps take the units in turn.  Eight lanes copy the 128 bytes of a row's
@@ -565,13 +543,17 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
         MoeSegment s;
         bool ok = true;
         const int swz = (row >> 1) & 3;   // 64-byte swizzle: 16-byte chunk c of row r lies at c ^ ((r >> 1) & 3)
+        bool holding = false;
+        auto let_go = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sc_empty(rs.s));
+            rs.step();
+            holding = false;
+        };
         auto take_chunk = [&]() {   // let go of the chunk held and wait for the next
-            if (held > 0) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sc_empty(rs.s));
-                rs.step();
-            }
+            if (holding) let_go();
             ++held;
+            holding = true;
             if (!wait(sc_full(rs.s), rs.ph)) ok = false;
             ok = __all_sync(~0u, ok);
         };
@@ -626,6 +608,8 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                 if (lane == 0) mbar_arrive(ready(r.s));
                 rc.step(G);
                 r.step(G);
+                // at once when the group's next unit is not in the chunk
+                if (dq_scales && (u + G >= s.k1 || (u + G) >> chunk_shift != u >> chunk_shift)) let_go();
             }
             before += units;
             chunk += static_cast<uint32_t>(((s.k1 - 1) >> chunk_shift) - first_chunk) + 1;
