@@ -126,6 +126,7 @@ int launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t stream) {
     g.swiglu = a.swiglu;
     g.wide_scales = g.nb % 8 == 0 && aligned(a.scales, 16);
     g.wide_zeros = g.zrow % 8 == 0 && aligned(a.zeros, 8);
+    g.copy_scales = g.nb % 4 == 0 && aligned(a.scales, 8) && (a.zeros == nullptr || g.wide_zeros);
     g.timeout_ns = call_options().wait_ns;
     g.status = gemm_status_word();
     g.bounds = bounds_counter();

@@ -58,6 +58,7 @@ struct MoeKernelArgs {
     int E, R, Tx, N, K, nb, zrow, gshift;   // group = 2^gshift
     int swiglu;
     int wide_scales, wide_zeros;   // rows of scales / zero points allow 16- / 8-byte loads
+    int copy_scales;               // rows of both allow 8-byte copies
     unsigned long long timeout_ns;
     unsigned int *status;
     unsigned int *bounds;
@@ -86,6 +87,9 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 // 16 bytes to shared memory, zeros where there is nothing to read.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool have) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(have ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
     asm volatile(

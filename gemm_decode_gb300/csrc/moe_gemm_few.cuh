@@ -234,20 +234,61 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
             }
         } else {
             // -------------------------------------------------------- scales and zero points
-            Ring<S::kScaleBufs> r;
+            // Each warp 64 rows, two per lane.  Where the rows allow 8-byte accesses a chunk is
+            // copied asynchronously, kAhead chunks before it is handed over: with groups of 32
+            // a chunk lasts four units, less than the latency of one load after another.
+            constexpr int kAhead = S::kScaleBufs - 2;
+            Ring<S::kScaleBufs> r, full;
+            int pending = 0;   // chunks copied and not handed over
             MoeSegment s;
             bool ok = true;
+            auto hand_over = [&]() {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sc_full(full.s));
+                full.step();
+                --pending;
+            };
             while (ok && next_segment<NT>(plan, s)) {
                 for (int c = s.k0 >> chunk_shift; c <= (s.k1 - 1) >> chunk_shift; ++c) {
-                    if (!wait(sc_empty(r.s), r.ph ^ 1u)) ok = false;
-                    ok = __all_sync(~0u, ok);
-                    if (!ok) break;
-                    load_scales<1>(g, s.expert, s.group * 128, c, warp & 1, lane, scale_ring + r.s * S::kScaleBytes);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sc_full(r.s));
-                    r.step();
+                    if (!__all_sync(~0u, mbar_test(sc_empty(r.s), r.ph ^ 1u))) {
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                        while (pending > 0) hand_over();
+                        if (!wait(sc_empty(r.s), r.ph ^ 1u)) ok = false;
+                        ok = __all_sync(~0u, ok);
+                        if (!ok) break;
+                    }
+                    unsigned char *buf = scale_ring + r.s * S::kScaleBytes;
+                    if (g.copy_scales) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int row = (warp & 1) * 64 + i * 32 + lane, n = s.group * 128 + row;
+                            const bool have = n < g.N;
+                            const int64_t at = static_cast<int64_t>(s.expert) * g.N + (have ? n : 0);
+                            const uint32_t to = smem_addr(buf + row * kScaleRow);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int j = c * kChunk + 4 * q;   // four groups
+                                const bool there = have && j < g.nb;
+                                copy8(to + 8 * q, g.scales + at * g.nb + (there ? j : 0), there);
+                            }
+                            if (dq_scales) copy8(to + 32, g.zeros + at * g.zrow + c * (kChunk / 2), have);
+                        }
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                        r.step();
+                        if (++pending > kAhead) {
+                            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+                            hand_over();
+                        }
+                    } else {
+                        load_scales<1>(g, s.expert, s.group * 128, c, warp & 1, lane, buf);
+                        r.step();
+                        ++pending;
+                        hand_over();
+                    }
                 }
             }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            while (pending > 0) hand_over();
         }
     } else if (warp < S::kXWarp) {
         // ------------------------------------------------------------ epilogue
