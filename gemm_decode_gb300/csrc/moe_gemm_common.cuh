@@ -44,7 +44,7 @@ constexpr int kChunk = 16;     // groups per row that the scale loader brings at
 constexpr int kSlotCols = 64;  // tensor-memory columns of 128 weights per lane
 constexpr int kTmemCols = 512;
 constexpr int kScaleRow = 40;  // bytes of a row's chunk: 16 scales, 8 bytes of zero points
-constexpr int kJoin = 14;      // units that joining partial sums takes as long as (measured: the break-even)
+constexpr int kJoin = 28;      // units that joining partial sums takes as long as (measured: see make_plan)
 
 struct MoeKernelArgs {
     const uint16_t *scales;

@@ -619,27 +619,20 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                 const unsigned char *codes = code_ring + rc.s * S::kCodeBytes + row * 64;
                 const unsigned char *sz = scale_ring + rs.s * S::kScaleBytes + row * kScaleRow + 32;
                 const uint32_t slot = slots + next % S::kSlots * kSlotCols;
-                uint4 c4[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) c4[q] = *reinterpret_cast<const uint4 *>(codes + ((q ^ swz) << 4));
                 // 32 codes of one group at a time (beyond K: zero codes, which nothing reads)
-                if (!dq_scales) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t out[16];
-                        decode32<true>(c4[q], 8u, __half2(), out);
-                        tmem_st16(slot + q * 16, out);
-                    }
-                } else {
-                    // the zero points of the unit's groups: nibbles from the unit's first on
+                uint32_t zz = 0x8888u;
+                if (dq_scales) {   // the zero points of the unit's groups: nibbles from the unit's first on
                     const int g0 = ((u * kUnit) >> g.gshift) % kChunk;
-                    const uint32_t zz = (*reinterpret_cast<const uint16_t *>(sz + (g0 >> 2) * 2)) >> (4 * (g0 & 3));
+                    zz = (*reinterpret_cast<const uint16_t *>(sz + (g0 >> 2) * 2)) >> (4 * (g0 & 3));
+                }
+                uint4 c = *reinterpret_cast<const uint4 *>(codes + (swz << 4));
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t out[16];
-                        decode32<true>(c4[q], (zz >> (((q * 32) >> g.gshift) * 4)) & 15u, __half2(), out);
-                        tmem_st16(slot + q * 16, out);
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const uint4 now = c;
+                    if (q < 3) c = *reinterpret_cast<const uint4 *>(codes + (((q + 1) ^ swz) << 4));
+                    uint32_t out[16];
+                    decode32<true>(now, (zz >> (((q * 32) >> g.gshift) * 4)) & 15u, __half2(), out);
+                    tmem_st16(slot + q * 16, out);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(code_empty(rc.s));
