@@ -149,7 +149,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
     };
     // bounded wait; false (and the abort flag) on expiry or when another role gave up
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (mbar_try(bar, parity)) return true;
+        if (limit != 0 ? mbar_try(bar, parity) : mbar_test(bar, parity)) return true;   // (try suspends)
         if (limit != 0) {
             const unsigned long long t0 = global_ns();
             for (;;) {
@@ -169,7 +169,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
             if (lane == 0) {
                 Ring<S::kCodeStages> r;
                 uint32_t issued = 0;
-                MoeSegment s;
+                MoeSegment s = {};
                 bool ok = true;
                 while (ok && next_segment<NT>(plan, s)) {
                     const int row = s.expert * g.N + s.group * 128;
@@ -194,7 +194,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
         } else if (warp == 1) {
             // -------------------------------------------------------- MMA
             Ring<S::kStages> r;
-            MoeSegment s;
+            MoeSegment s = {};
             bool ok = true;
             const uint64_t x_desc = umma_desc(smem_addr(x_ring));
             auto segment = [&](auto per_group) {
@@ -240,7 +240,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
             constexpr int kAhead = S::kScaleBufs - 2;
             Ring<S::kScaleBufs> r, full;
             int pending = 0;   // chunks copied and not handed over
-            MoeSegment s;
+            MoeSegment s = {};
             bool ok = true;
             auto hand_over = [&]() {
                 __syncwarp();
@@ -307,7 +307,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
             for (uint32_t n = 0; n < sets; ++n)   // every set is free
                 if (lane == 0) mbar_arrive(ready(n));
         uint32_t before = 0, chunk = 0;   // units and chunks of earlier segments
-        MoeSegment s;
+        MoeSegment s = {};
         int buf = 0;
         bool ok = true;
         float sum[NT];
@@ -465,7 +465,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
             float *mine = slot_of(blockIdx.x);
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                if (j < s.rows) mine[j * 128] = sum[j];
+                if (j < s.rows && ib(mine + j * 128 < g.partial + static_cast<int64_t>(2 * gridDim.x) * 128 * NT)) mine[j * 128] = sum[j];
             __threadfence();
             sync4();
             if (t == 0) last_flag[me] = atomicAdd(g.arrived + c0, 1u) == c1 - c0;
@@ -500,7 +500,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
         r.step(me);
         int full = -1;     // stage whose copies are in flight
         uint32_t next = static_cast<uint32_t>(me), before = 0;   // the warp's next unit; units of earlier segments
-        MoeSegment s;
+        MoeSegment s = {};
         bool ok = true;
         const int chunk = lane & 7, sub = lane >> 3;
         const uint32_t x_base = smem_addr(x_ring);
@@ -545,6 +545,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                 const __half *from = g.xparts + (have0 ? k : 0);
 #pragma unroll 4
                 for (int j = sub; j < n16; j += 4) {
+                    if (!ib(list[j] >= 0 && list[j] <= g.Tx && r.s * S::kXBytes + 2 * S::kXHalf <= S::kStages * S::kXBytes)) continue;
                     const __half *row = from + static_cast<int64_t>(list[j]) * g.K;
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p) {   // the second part's rows follow the first's
@@ -581,7 +582,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
         r.step(me);
         uint32_t next = static_cast<uint32_t>(me), before = 0;   // the group's next unit; units of earlier segments
         uint32_t chunk = 0, held = 0;                            // chunks of earlier segments; chunks taken so far
-        MoeSegment s;
+        MoeSegment s = {};
         bool ok = true;
         const int swz = (row >> 1) & 3;   // 64-byte swizzle: 16-byte chunk c of row r lies at c ^ ((r >> 1) & 3)
         bool holding = false;

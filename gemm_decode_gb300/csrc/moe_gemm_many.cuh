@@ -140,7 +140,7 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
     };
     // bounded wait; false (and the abort flag) on expiry or when another role gave up
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (mbar_try(bar, parity)) return true;
+        if (limit != 0 ? mbar_try(bar, parity) : mbar_test(bar, parity)) return true;   // (try suspends)
         if (limit != 0) {
             const unsigned long long t0 = global_ns();
             for (;;) {
@@ -158,7 +158,7 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
         if (lane == 0) {
             Ring<S::kCodeStages> r;
             int64_t issued = 0;
-            MoeSegment s;
+            MoeSegment s = {};
             bool ok = true;
             while (ok && next_segment<NT>(plan, s)) {
                 const int row = s.expert * g.N + s.group * (128 * RT);
@@ -187,7 +187,7 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
         Ring<S::kXStages> rx;
         Ring<S::kSlots> ra;
         uint32_t d_ph = 0;
-        MoeSegment s;
+        MoeSegment s = {};
         bool ok = true;
         const uint64_t x_desc = umma_desc(smem_addr(x_ring));
         const int half_unit = g.K % kUnit != 0 && g.K % kUnit <= kHalf ? g.K / kUnit : -1;   // the unit of one half
@@ -240,7 +240,7 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
     } else {
         // ------------------------------------------------------------ scales and zero points
         Ring<S::kScaleBufs> r;
-        MoeSegment s;
+        MoeSegment s = {};
         bool ok = true;
         while (ok && next_segment<NT>(plan, s)) {
             for (int c = s.k0 >> (g.gshift - 3); c <= (s.k1 - 1) >> (g.gshift - 3); ++c) {   // 2^(gshift - 3) units each
@@ -278,7 +278,7 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
             *p = __float2bfloat16_rn(v);
         };
         uint32_t d_ph = 0;
-        MoeSegment s;
+        MoeSegment s = {};
         int buf = 0;
         // 16 columns (rows of x from j0 on) of weight row n, unscaled sums in v
         auto finish = [&](int n, int j0, const float *v, const float *scale) {
@@ -333,7 +333,9 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        if (j0 + j < s.rows) mine[(j0 + j) * 128] = v[j];
+                        if (j0 + j < s.rows &&
+                            ib(mine + (j0 + j) * 128 < g.partial + static_cast<int64_t>(2 * gridDim.x) * RT * 128 * NT))
+                            mine[(j0 + j) * 128] = v[j];
                 }
             };
             const uint32_t acc0 = tmem + lane_base + static_cast<uint32_t>(rt * NT);
@@ -385,7 +387,7 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
         r.step(me % S::kXStages);
         int full = -1;     // stage whose copies are in flight
         uint32_t next = static_cast<uint32_t>(me), before = 0;   // the warp's next unit; units of earlier segments
-        MoeSegment s;
+        MoeSegment s = {};
         bool ok = true;
         const int chunk = lane & 7, sub = lane >> 3;
         const uint32_t x_base = smem_addr(x_ring);
@@ -430,6 +432,7 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
                 const __half *from = g.xparts + (have0 ? k : 0);
 #pragma unroll 4
                 for (int j = sub; j < n16; j += 4) {
+                    if (!ib(list[j] >= 0 && list[j] <= g.Tx)) continue;
                     const __half *row = from + static_cast<int64_t>(list[j]) * g.K;
                     const uint32_t to = dst + sw128_offset(j, chunk);
                     copy16(to, row, have0);
@@ -462,10 +465,9 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
         uint32_t next = static_cast<uint32_t>(group_id), before = 0;   // the next job; jobs of earlier segments
         uint32_t chunk = 0, held = 0;                                  // chunks of earlier segments; chunks taken so far
         uint32_t unit_at = 0;                                          // unit whose codes are at rc
-        MoeSegment s;
+        MoeSegment s = {};
         bool ok = true;
         const int chunk_shift = g.gshift - 3;
-        const int half_unit = g.K % kUnit != 0 && g.K % kUnit <= kHalf ? g.K / kUnit : -1;   // the unit of one half
         const int swz = (row >> 1) & 3;   // 64-byte swizzle: 16-byte chunk c of row r lies at c ^ ((r >> 1) & 3)
         auto take_chunk = [&]() {   // let go of the chunk held and wait for the next
             if (held > 0) {

@@ -412,3 +412,61 @@ def test_block_equals_its_parts(torch, bf16, T, E, k, H, inner, g):
     for p, q in ((ids, ids2), (w, w2), (out, out2), (nrm, nrm2)):
         assert torch.equal(p, q)
     assert torch.isfinite(out).all() and torch.isfinite(nrm).all()
+
+
+# ---------------------------------------------------------------- bounded waits, checked indexes
+
+@pytest.mark.parametrize("bf16,T", [(False, 9), (False, 200), (True, 9), (True, 200)])
+def test_experts_bounded_wait_reports_timeout_without_fault(torch, bf16, T):
+    """A zero bound makes the pipelines give up; the context and the next call are sound."""
+    rng = np.random.default_rng(T)
+    weights = make_weights(rng, 4, 300, 1024, 64, False)
+    offsets, rows = groups(rng, 4, 2, T, "even")
+    x = num(torch.from_numpy(rng.normal(0, 1, (T, 1024))).to(torch.bfloat16 if bf16 else torch.float32))
+    t = torch.bfloat16 if bf16 else torch.float32
+    args = [to(torch, a) for a in weights] + [to(torch, x, t), to(torch, rows), to(torch, offsets)]
+    y = torch.zeros(2 * T, 300, dtype=t, device="cuda")
+    ws = work(torch, q4.q4moe_gemm_workspace(2 * T, T, 300, 1024, 4, t))
+    q4.q4moe_gemm_run(*args, y, ws, group=64, wait_timeout_ns=0)
+    torch.cuda.synchronize()
+    assert q4.q4gemv_device_status() == q4.Q4_ERR_TIMEOUT
+    assert q4.q4gemv_device_status() == q4.Q4_OK        # reported once
+    q4.q4moe_gemm_run(*args, y, ws, group=64)
+    torch.cuda.synchronize()
+    want, bound = ref.experts(ref.dequant(*weights, 64), x, rows, offsets, np.zeros((2 * T, 300)), False, bf16)
+    within(num(y), want, bound, "after the timeout")
+
+
+@pytest.fixture(scope="module")
+def checking(torch):
+    """The bounds-checking build in the library's place."""
+    from gemm_decode_gb300 import build as q4build
+    path = q4build.build(variant="check")
+    saved = q4._lib, q4.library_path
+    q4._lib, q4.library_path = None, lambda: path
+    try:
+        assert q4.q4gemv_bounds_violations() == 0
+        yield
+    finally:
+        q4._lib, q4.library_path = saved
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("E,k,T,N,K,g", [(9, 2, 70, 330, 416, 32), (4, 2, 5, 257, 2112, 64), (2, 1, 300, 514, 896, 128)])
+def test_experts_stay_in_bounds(torch, checking, bf16, E, k, T, N, K, g):
+    check_experts(torch, E, E, k, T, N, K, g, False, False, bf16, shape="holes")
+    assert q4.q4gemv_bounds_violations() == 0
+
+
+# ---------------------------------------------------------------- the example
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_example_block(torch, dtype):
+    """The example's block against a plain one, for a prompt and for single tokens in a graph."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import moe_block
+    worst = moe_block.check(getattr(torch, dtype), hidden=512, inner=256, experts=8, top_k=2, group=64)
+    # bfloat16: the rows inside an expert and its output are rounded too (2^-8 half steps each)
+    assert worst <= (4 * ref.UBF if dtype == "bfloat16" else 1e-5)
