@@ -15,8 +15,9 @@
 // second launch adds the histograms of the blocks before it.  No atomics: the order is
 // the same on every run.
 //
-// Bound: latency for decoding (the k dependent rounds of one warp and two block
-// barriers), the logits' bytes for long prompts.
+// Bound: latency (the k dependent rounds of one warp, the block barriers, the second launch).
+// Measured: one token, 8 of 64 experts 3.1 us; 8191 tokens, 8 of 128 experts 16.5 us (20.4
+// with blocks of 1024 choices and no logits fetched ahead).
 #include "q4_moe.cuh"
 
 namespace q4 {

@@ -387,11 +387,12 @@ Q4_API int64_t q4moe_gemm_workspace(int64_t R, int64_t Tx, int64_t N, int64_t K,
  * Rows of y that no expert owns are left as they were.  Each offset is clamped to [0, R]
  * and to no less than the one before it, and a row index outside [0, Tx) reads as a row of
  * zeros, so no content of the two arrays makes the kernels leave their buffers.
- * Accuracy: binary32 sums; for Q4_F32 weights and activations are each carried as two
- * binary16 parts (22 bits and more), for Q4_BF16 the activations are exact and each weight
- * is rounded once to binary16.  |(q - z) s| < 65504 and finite x, as in the tensor-core
- * GEMV; each row of x is scaled by its own power of two, so its range is not limited.
- * 1 <= E <= 1024, R and Tx < 2^31, E * N < 2^31 (Q4_ERR_UNSUPPORTED above). */
+ * Accuracy: binary32 sums.  Q4_F32: activations to 22 bits (two binary16 parts), weights
+ * exact.  Q4_BF16: activations exact, weights exact up to 24 rows per expert on average and
+ * rounded once to binary16 above (then |(q - z) s| < 65504, as in the tensor-core GEMV).
+ * Each row of x is scaled by its own power of two, so its range is not limited; a row with
+ * a NaN or infinity gives non-finite outputs in that row alone.
+ * 1 <= E <= 1024, R and Tx < 2^31, E * N < 2^31, K <= 2^26 (Q4_ERR_UNSUPPORTED above). */
 Q4_API int q4moe_gemm_run(const void *codes, const void *scales_f16, const void *zeros_u4_or_null, const void *x,
                    const int32_t *rows_or_null, const int32_t *offsets, void *y, int32_t E, int64_t R, int64_t Tx,
                    int64_t N, int64_t K, int32_t group, int32_t dtype, int32_t epilogue, void *workspace,
