@@ -32,7 +32,7 @@
 // and binary16 arithmetic together issue 2.5 warp instructions per clock and SM (measured),
 // so dequantisation alone takes 250 cycles per unit, where HBM would deliver one in 360; with
 // the other roles beside it a unit takes about 730.  Measured: 8 experts of 28672 x 4096
-// (groups of 128), 48 tokens bfloat16: 145 us, 3.4 TB/s (0.50 of measured).  Scaled weights
+// (groups of 128), 48 tokens bfloat16: 144 us, 3.4 TB/s (0.50 of measured).  Scaled weights
 // and one sum over K, as in moe_gemm_many.cuh, took 152 us there; one epilogue group for all
 // units 187 us; two MMA warps 160 us.
 #pragma once
@@ -359,7 +359,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                             }
                         }
                 } else {
-#pragma unroll
+#pragma unroll 1   // (straight-line code would crowd the instruction cache)
                     for (int i = 0; i < MG; i += 2)   // two groups, their loads in flight together
                         if (i < groups) {
                             const bool two = i + 1 < groups;
@@ -547,7 +547,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                 const uint32_t dst = x_base + r.s * S::kXBytes;
                 const bool have0 = k < g.K, have1 = k + kHalf < g.K;
                 const __half *from = g.xparts + (have0 ? k : 0);
-#pragma unroll 4
+#pragma unroll 2
                 for (int j = sub; j < n16; j += 4) {
                     if (!ib(list[j] >= 0 && list[j] <= g.Tx && r.s * S::kXBytes + 2 * S::kXHalf <= S::kStages * S::kXBytes)) continue;
                     const __half *row = from + static_cast<int64_t>(list[j]) * g.K;

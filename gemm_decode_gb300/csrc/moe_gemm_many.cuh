@@ -23,7 +23,7 @@
 // What bounds it: the tensor core is busy 1024 of about 2400 cycles per unit; the rest is the
 // issuing warp's own steps between runs of MMAs, and 0.17 of the time the wait for the
 // epilogue at an item's end.  Measured: 4096 tokens, 8 of 64 experts of 2048 x 2048 (groups
-// of 64, SwiGLU): 307 us, 895 TFLOP/s (0.47 of measured bf16).  A fourth dequantiser group
+// of 64, SwiGLU): 302 us, 911 TFLOP/s (0.48 of measured bf16).  A fourth dequantiser group
 // (310 us) and an MMA warp per weight tile (323 us, with registers spilled) gained nothing.
 #pragma once
 
