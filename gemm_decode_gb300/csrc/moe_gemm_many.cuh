@@ -182,11 +182,12 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
                     ++issued;
                 }
             }
-            // (on abort) every copy in flight lands before the CTA may exit
-            if (*abort_flag)
-                for (int64_t j = issued > S::kCodeStages ? issued - S::kCodeStages : 0; j < issued; ++j)
-                    mbar_wait(code_full(static_cast<int>(j % S::kCodeStages)),
-                              static_cast<uint32_t>(j / S::kCodeStages) & 1u, 50ull * 1000 * 1000);
+            // Every copy lands before the CTA may exit, whichever role gives up, and when: a
+            // flag read here could be raised a moment later.  (Otherwise the copies are waited
+            // for anyway, by the dequantisers.)
+            for (int64_t j = issued > S::kCodeStages ? issued - S::kCodeStages : 0; j < issued; ++j)
+                mbar_wait(code_full(static_cast<int>(j % S::kCodeStages)),
+                          static_cast<uint32_t>(j / S::kCodeStages) & 1u, 50ull * 1000 * 1000);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA

@@ -1,0 +1,28 @@
+"""A kernel that gives up on a bounded wait must not leave its bulk copies in flight: they
+would land in shared memory that the next CTA owns.  Any role may give up at any moment, so
+the copying lane waits for its copies whether or not a flag is raised when it looks.
+
+Read from the sources: the race needs a wait that expires while a copy is under way, which no
+run shows reliably.
+"""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gemm_decode_gb300", "csrc")
+FLAG = r"if \((?:\*abort_flag|aborted\(\))\)"
+COMMENT = r"(?:\s|//[^\n]*\n)*"
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+@pytest.mark.parametrize("name", ["moe_gemm_few.cuh", "moe_gemm_many.cuh"])
+def test_copies_are_drained_whatever_the_flag(name):
+    text = source(name)
+    drain = re.search(r"for \([^;]*issued[^;]*;[^;]*issued; \+\+\w+\)" + COMMENT + r"mbar_wait\(", text)
+    assert drain, "the copying lane waits for the copies it issued"
+    assert not re.search(FLAG + COMMENT + r"\{?" + COMMENT + r"for \([^;]*issued", text), "the drain depends on a flag"
