@@ -151,11 +151,10 @@ q4gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a, const GemmArgs g) {
                                 m0 + h * BM);
                 issued = kb + 1;
             }
-            if (*abort_flag) {
-                // drain (bounded): every issued tile lands before the CTA may exit
-                for (int kb = issued - STAGES > 0 ? issued - STAGES : 0; kb < issued; ++kb)
-                    mbar_wait(full_a(kb % STAGES), (kb / STAGES) & 1, 50ull * 1000 * 1000);
-            }
+            // Drain (bounded): every issued tile lands before the CTA may exit, whichever role
+            // gives up, and when (a flag read here could be raised a moment later).
+            for (int kb = issued - STAGES > 0 ? issued - STAGES : 0; kb < issued; ++kb)
+                mbar_wait(full_a(kb % STAGES), (kb / STAGES) & 1, 50ull * 1000 * 1000);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -311,8 +310,9 @@ q4gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a, const GemmArgs g) {
         }
     }
     // ---- teardown: make sure every issued MMA finished before TMEM is released ----
-    if (warp == 1 && lane == 0 && *abort_flag) {
-        // drain (bounded): the commit on done_bar tracks all MMAs this thread issued
+    if (warp == 1 && lane == 0) {
+        // drain (bounded): the commit on done_bar tracks all MMAs this thread issued; waited
+        // for whichever role gave up, and when
         mbar_wait(done_bar, 0, 50ull * 1000 * 1000);
     }
     tc_fence_before();

@@ -171,11 +171,10 @@ q4gemm_split_kernel(const __grid_constant__ CUtensorMap tmap_a, const SplitArgs 
                 tma_load_2d(smem_addr(tiles_a + s * kATileS), &tmap_a, full_a(s), (kb_begin + j) * SBK, m0);
                 issued = j + 1;
             }
-            if (*abort_flag) {
-                // drain (bounded): every issued tile lands before the CTA may exit
-                for (int j = issued - kSplitStages > 0 ? issued - kSplitStages : 0; j < issued; ++j)
-                    mbar_wait(full_a(j % kSplitStages), (j / kSplitStages) & 1, 50ull * 1000 * 1000);
-            }
+            // Drain (bounded): every issued tile lands before the CTA may exit, whichever role
+            // gives up, and when (a flag read here could be raised a moment later).
+            for (int j = issued - kSplitStages > 0 ? issued - kSplitStages : 0; j < issued; ++j)
+                mbar_wait(full_a(j % kSplitStages), (j / kSplitStages) & 1, 50ull * 1000 * 1000);
         }
         __syncwarp();
         if (split > 1) cluster_wait();
@@ -361,7 +360,7 @@ q4gemm_split_kernel(const __grid_constant__ CUtensorMap tmap_a, const SplitArgs 
         }
     }
     // ---- teardown: every issued MMA finished before TMEM is released ----
-    if (warp == 1 && lane == 0 && *abort_flag) mbar_wait(done_bar, 0, 50ull * 1000 * 1000);
+    if (warp == 1 && lane == 0) mbar_wait(done_bar, 0, 50ull * 1000 * 1000);   // whichever role gave up, and when
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {

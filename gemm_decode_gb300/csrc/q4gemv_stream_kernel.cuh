@@ -182,11 +182,10 @@ q4gemv_stream_kernel(const StreamArgsOf<FUSE> a) {
                     ph ^= 1;
                 }
             }
-            if (aborted()) {
-                // drain (bounded): every issued copy lands before the CTA may exit
-                for (int i = issued - D > 0 ? issued - D : 0; i < issued; ++i)
-                    mbar_wait(full(i % D), (i / D) & 1, 50ull * 1000 * 1000);
-            }
+            // Drain (bounded): every issued copy lands before the CTA may exit, whichever role
+            // gives up, and when (a flag read here could be raised a moment later).
+            for (int i = issued - D > 0 ? issued - D : 0; i < issued; ++i)
+                mbar_wait(full(i % D), (i / D) & 1, 50ull * 1000 * 1000);
         }
         return;
     }

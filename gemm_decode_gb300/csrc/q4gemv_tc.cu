@@ -217,11 +217,10 @@ q4gemv_tc_kernel(const __grid_constant__ CUtensorMap tmap_codes, const TcArgs g)
                 }
                 issued = j + 1;
             }
-            if (*abort_flag) {
-                // drain (bounded): every issued box lands before the CTA may exit
-                for (int j = issued - CST > 0 ? issued - CST : 0; j < issued; ++j)
-                    mbar_wait(cfull(j % CST), (j / CST) & 1, 50ull * 1000 * 1000);
-            }
+            // Drain (bounded): every issued box lands before the CTA may exit, whichever role
+            // gives up, and when (a flag read here could be raised a moment later).
+            for (int j = issued - CST > 0 ? issued - CST : 0; j < issued; ++j)
+                mbar_wait(cfull(j % CST), (j / CST) & 1, 50ull * 1000 * 1000);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -555,7 +554,7 @@ q4gemv_tc_kernel(const __grid_constant__ CUtensorMap tmap_codes, const TcArgs g)
         cluster.sync();   // peers' shared memory stays valid until every read is done
     }
     // ---- teardown: every issued MMA finished before TMEM is released ----
-    if (warp == 1 && lane == 0 && *abort_flag) mbar_wait(done_bar, 0, 50ull * 1000 * 1000);
+    if (warp == 1 && lane == 0) mbar_wait(done_bar, 0, 50ull * 1000 * 1000);   // whichever role gave up, and when
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {

@@ -20,9 +20,20 @@ def source(name):
         return f.read()
 
 
-@pytest.mark.parametrize("name", ["moe_gemm_few.cuh", "moe_gemm_many.cuh"])
+@pytest.mark.parametrize("name", ["moe_gemm_few.cuh", "moe_gemm_many.cuh", "q4gemm.cu", "q4gemm_split.cu",
+                                  "q4gemv_tc.cu", "q4gemv_stream_kernel.cuh"])
 def test_copies_are_drained_whatever_the_flag(name):
     text = source(name)
     drain = re.search(r"for \([^;]*issued[^;]*;[^;]*issued; \+\+\w+\)" + COMMENT + r"mbar_wait\(", text)
     assert drain, "the copying lane waits for the copies it issued"
     assert not re.search(FLAG + COMMENT + r"\{?" + COMMENT + r"for \([^;]*issued", text), "the drain depends on a flag"
+
+
+@pytest.mark.parametrize("name", ["q4gemm.cu", "q4gemm_split.cu", "q4gemv_tc.cu"])
+def test_tensor_memory_is_freed_behind_the_last_product(name):
+    """The same for the products still writing the tensor memory that a CTA frees as it ends."""
+    text = source(name)
+    teardown = text.rindex("mbar_wait(done_bar, 0")
+    assert teardown < text.index("tcgen05.dealloc")
+    condition = text[text.rindex("if (", 0, teardown):teardown]
+    assert "warp == 1 && lane == 0" in condition and "abort_flag" not in condition
