@@ -25,7 +25,7 @@ __all__ = [
     "q4gemv_bounds_violations", "q4gemv_grouped_split",
     "q4moe_route_run", "q4moe_route_workspace", "q4moe_gemm_run", "q4moe_gemm_workspace",
     "q4_block_norm_run", "q4moe_block_run", "q4moe_block_workspace",
-    "Q4_F32", "Q4_BF16", "Q4_ROUTE_SOFTMAX", "Q4_ROUTE_SIGMOID",
+    "Q4_F32", "Q4_BF16", "Q4_ROUTE_SOFTMAX", "Q4_ROUTE_SIGMOID", "Q4_ROUTE_SCORE_BIAS",
     "Q4_OK", "Q4_ERR_INVALID_ARG", "Q4_ERR_UNSUPPORTED", "Q4_ERR_MISALIGNED",
     "Q4_ERR_CUDA", "Q4_ERR_TIMEOUT", "Q4_EPILOGUE_NONE", "Q4_EPILOGUE_SWIGLU",
     "Q4_RUN_OVERLAPPED", "Q4_RUN_EXACT_X", "Q4_RUN_WAIT_TIMEOUT",
@@ -39,7 +39,7 @@ Q4_OK, Q4_ERR_INVALID_ARG, Q4_ERR_UNSUPPORTED, Q4_ERR_MISALIGNED, Q4_ERR_CUDA, Q
 Q4_EPILOGUE_NONE, Q4_EPILOGUE_SWIGLU = 0, 1
 Q4_RUN_OVERLAPPED, Q4_RUN_EXACT_X, Q4_RUN_WAIT_TIMEOUT = 0x1, 0x2, 0x4
 Q4_F32, Q4_BF16 = 0, 1
-Q4_ROUTE_SOFTMAX, Q4_ROUTE_SIGMOID = 0, 1
+Q4_ROUTE_SOFTMAX, Q4_ROUTE_SIGMOID, Q4_ROUTE_SCORE_BIAS = 0, 1, 0x10
 
 
 def library_path() -> str:
@@ -535,7 +535,10 @@ def q4moe_block_workspace(T, E, top_k, H, inner, dtype) -> int:
 def q4moe_route_run(logits, ids, weights, offsets, rows, pos, workspace, bias=None, token_mask=None,
                     score=Q4_ROUTE_SOFTMAX, renormalize=True, scale=1.0, flags=None, stream=None, check=True) -> int:
     """The top_k experts of each token (ids [T, top_k], weights), and the rows grouped by
-    expert (offsets [E + 1], rows [T * top_k], pos [T, top_k])."""
+    expert (offsets [E + 1], rows [T * top_k], pos [T, top_k]).  bias [E] enters the choice
+    only: added to the logits, or, with score=Q4_ROUTE_SIGMOID | Q4_ROUTE_SCORE_BIAS (or
+    SOFTMAX), to the scores, as the balancing bias of a model trained without an auxiliary
+    loss is."""
     if _Types.f32 is None:
         _Types.load()
     T, E = logits.shape

@@ -16,6 +16,9 @@ bool valid_dtype(int32_t d) { return d == Q4_F32 || d == Q4_BF16; }
 int64_t size_of(int32_t d) { return d == Q4_BF16 ? 2 : 4; }
 bool finite_nonneg(float v) { return v >= 0.0f && v <= 3.0e38f; }   // NaN fails too
 
+bool is_sigmoid(int32_t score) { return (score & ~Q4_ROUTE_SCORE_BIAS) == Q4_ROUTE_SIGMOID; }
+bool is_score_bias(int32_t score) { return (score & Q4_ROUTE_SCORE_BIAS) != 0; }
+
 // Outputs against inputs and against one another.
 bool outputs_clash(const Span *out, int nout, const Span *in, int nin) {
     for (int i = 0; i < nout; ++i) {
@@ -27,7 +30,8 @@ bool outputs_clash(const Span *out, int nout, const Span *in, int nin) {
 
 int route_shape(int64_t T, int64_t E, int64_t k, int32_t score) {
     if (T < 0 || E < 1 || k < 1 || k > E) return Q4_ERR_INVALID_ARG;
-    if (score != Q4_ROUTE_SOFTMAX && score != Q4_ROUTE_SIGMOID) return Q4_ERR_INVALID_ARG;
+    const int32_t kind = score & ~Q4_ROUTE_SCORE_BIAS;
+    if (kind != Q4_ROUTE_SOFTMAX && kind != Q4_ROUTE_SIGMOID) return Q4_ERR_INVALID_ARG;
     if (E > kMaxExperts || k > kMaxTopK || T * k > 0x7fffffffLL) return Q4_ERR_UNSUPPORTED;
     return Q4_OK;
 }
@@ -123,8 +127,8 @@ int q4moe_route_run(const float *logits, const float *bias_or_null, const uint8_
         if (outputs_clash(out, 6, in, 3)) return Q4_ERR_INVALID_ARG;
     }
     CallScope scope(co);
-    RouteArgs a = {logits, bias_or_null, token_mask_or_null, T, E, top_k, score == Q4_ROUTE_SIGMOID,
-                   renormalize != 0, scale, ids, weights, offsets, rows, pos, static_cast<int *>(workspace)};
+    RouteArgs a = {logits, bias_or_null, token_mask_or_null, T, E, top_k, is_sigmoid(score), renormalize != 0,
+                   is_score_bias(score), scale, ids, weights, offsets, rows, pos, static_cast<int *>(workspace)};
     return launch_route(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -260,8 +264,8 @@ int q4moe_block_run(const q4moe_block_t *args, const q4_run_options_t *opts, voi
     int *offsets = reinterpret_cast<int *>(w + l.offsets), *rows = reinterpret_cast<int *>(w + l.rows),
         *pos = reinterpret_cast<int *>(w + l.pos);
     const RouteArgs r = {g.logits, g.bias_or_null, g.token_mask_or_null, g.T, g.E, g.top_k,
-                         g.score == Q4_ROUTE_SIGMOID, g.renormalize != 0, g.route_scale, g.ids, g.route_weights,
-                         offsets, rows, pos, reinterpret_cast<int *>(w + l.scratch)};
+                         is_sigmoid(g.score), g.renormalize != 0, is_score_bias(g.score), g.route_scale, g.ids,
+                         g.route_weights, offsets, rows, pos, reinterpret_cast<int *>(w + l.scratch)};
     if ((st = launch_route(r, cs)) != Q4_OK) return st;
     OverlapInside inside;
     const int bf16 = g.dtype == Q4_BF16;

@@ -5,7 +5,8 @@
 // 32-bit key that orders as the binary32 value does (0: never chosen), so a round of the
 // choice is one integer maximum over the warp and one minimum over the indices that hold
 // it -- exact, with ties to the lower expert, and without a floating-point comparison of
-// rounded scores: softmax and sigmoid rise with the logit, so the choice never needs them.
+// rounded scores: softmax and sigmoid rise with the logit, so the choice needs them only
+// where a bias is added to the score itself.
 //
 // The grouped order is a counting sort that keeps the order of the tokens.  A block of
 // 512 choices counts them per warp with one match over the warp (the rank inside the
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
         int mine = -1;   // lane j: the token's j-th choice
         float m_all = -INFINITY, s_all = 0.0f;
         if (live) {
-            if (!a.sigmoid && !a.renorm) {
+            const bool on_score = a.score_bias != 0 && a.bias != nullptr;
+            if (!a.sigmoid && (!a.renorm || on_score)) {
 #pragma unroll
                 for (int c = 0; c < NV; ++c) m_all = fmaxf(m_all, v[c]);
                 m_all = warp_max(m_all);
@@ -127,7 +129,11 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
             for (int c = 0; c < NV; ++c) {
                 const int e = c * 32 + lane;
                 const float b = a.bias != nullptr && e < a.E ? a.bias[e] : 0.0f;
-                key[c] = choice_key(a.bias != nullptr ? v[c] + b : v[c]);
+                float sel = v[c];
+                // (an expert whose logit is -inf stays out, whatever its bias)
+                if (on_score && v[c] > -INFINITY)
+                    sel = a.sigmoid ? 1.0f / (1.0f + expf(-v[c])) : expf(v[c] - m_all) / s_all;
+                key[c] = choice_key(a.bias != nullptr ? sel + b : sel);
                 best = max(best, key[c]);
             }
             for (int j = 0; j < a.k; ++j) {

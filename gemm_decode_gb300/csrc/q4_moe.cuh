@@ -14,7 +14,7 @@ struct RouteArgs {
     const float *logits, *bias;
     const uint8_t *mask;
     int T, E, k;
-    int sigmoid, renorm;
+    int sigmoid, renorm, score_bias;   // score_bias: the bias is added to the score, not to the logit
     float scale;
     int *ids;
     float *weights;

@@ -344,14 +344,19 @@ Q4_API int q4gemv_set_overlapped_launch(int enable);
 #define Q4_BF16 1
 #define Q4_ROUTE_SOFTMAX 0
 #define Q4_ROUTE_SIGMOID 1
+#define Q4_ROUTE_SCORE_BIAS 0x10   /* or-ed to either: the bias is added to the score */
 
 /* Bytes of workspace q4moe_route_run needs (-1 for sizes it does not serve). */
 Q4_API int64_t q4moe_route_workspace(int32_t T, int32_t E, int32_t top_k);
 
 /* Router: each token's top_k experts, their weights, and the rows grouped by expert.
- *   sel[t][e] = logits[t][e] + bias[e] (one binary32 addition; bias NULL: the logit)
+ *   sel[t][e] = logits[t][e] + bias[e] (one binary32 addition; bias NULL: the logit), or,
+ *   with Q4_ROUTE_SCORE_BIAS,
+ *   sel[t][e] = p + bias[e], p the expert's binary32 score: 1 / (1 + exp(-l_e)) or
+ *   exp(l_e) / sum exp(l) over all experts.  The two order experts differently: the
+ *   bias that balances a router without an auxiliary loss is one on the score.
  *   The top_k largest sel are chosen in descending order, equal ones by lower expert.
- *   An expert whose sel is NaN or -inf is never chosen, nor is any by a token whose
+ *   An expert whose logit or sel is NaN or -inf is never chosen, nor is any by a token whose
  *   token_mask byte is 0: the places left over hold id -1, weight 0 and pos -1.
  *   Weights, from the logits without the bias (logits finite, -inf or NaN; NaN counts as
  *   -inf), S the token's chosen experts:
