@@ -11,7 +11,10 @@
 //
 // x.  A first kernel (moe_prepare_kernel) writes each row of x as binary16 parts of x 2^e
 // with 2^14 <= max |x| 2^e < 2^15: one part carries bfloat16 exactly, two carry binary32 to
-// 22 bits, whatever the row's range.  (q - z) is exact in binary16.
+// 22 bits, as long as the parts stay above binary16's last step, 2^-24; half of that step,
+// 2^-39 of the row's largest element, is lost of anything smaller.  (A power of two per unit
+// of k would follow outliers closer, at a multiplication per sum and unit in the epilogue.)
+// (q - z) is exact in binary16.
 //
 // Codes.  A word of eight codes in natural order yields the pairs (0,4), (1,5), (2,6), (3,7)
 // with one logic operation each; the prepared x has its elements in that order.

@@ -392,11 +392,15 @@ Q4_API int64_t q4moe_gemm_workspace(int64_t R, int64_t Tx, int64_t N, int64_t K,
  * Rows of y that no expert owns are left as they were.  Each offset is clamped to [0, R]
  * and to no less than the one before it, and a row index outside [0, Tx) reads as a row of
  * zeros, so no content of the two arrays makes the kernels leave their buffers.
- * Accuracy: binary32 sums.  Q4_F32: activations to 22 bits (two binary16 parts), weights
- * exact.  Q4_BF16: activations exact, weights exact up to 24 rows per expert on average and
- * rounded once to binary16 above (then |(q - z) s| < 65504, as in the tensor-core GEMV).
- * Each row of x is scaled by its own power of two, so its range is not limited; a row with
- * a NaN or infinity gives non-finite outputs in that row alone.
+ * Accuracy: sums in binary32; before them
+ *   Q4_F32: activations to 2^-22 |x_k| + 2^-39 max |x| of the row, weights exact;
+ *   Q4_BF16: activations to 2^-39 max |x| of the row (exact down to 2^-31 of it), weights
+ *   exact up to 24 rows per expert on average, above that rounded once to binary16:
+ *   2^-11 |w| + 2^-25, and |(q - z) s| < 65504, as in the tensor-core GEMV.
+ * The elements of a row share one power of two: the row as a whole may have any size, but
+ * elements more than 2^17 (Q4_F32) or 2^31 (Q4_BF16) below its largest keep only what the
+ * absolute term leaves of them.  A row with a NaN or infinity gives non-finite outputs in
+ * that row alone.
  * 1 <= E <= 1024, R and Tx < 2^31, E * N < 2^31, K <= 2^26 (Q4_ERR_UNSUPPORTED above). */
 Q4_API int q4moe_gemm_run(const void *codes, const void *scales_f16, const void *zeros_u4_or_null, const void *x,
                    const int32_t *rows_or_null, const int32_t *offsets, void *y, int32_t E, int64_t R, int64_t Tx,

@@ -56,3 +56,21 @@ def test_bfloat16_weights_are_exact_up_to_24_rows_per_expert(torch, K, g):
     got, want, _ = products(torch, K, 2, 2, 20, 800, K, g, False, False, True)
     rounded = num(torch.from_numpy(want).to(torch.bfloat16))
     assert float((got != rounded).mean()) <= mb.MISROUNDED
+
+
+@pytest.mark.parametrize("bf16,T,outlier", [(False, 5, 1e5), (False, 40, 1e9), (True, 5, 2.0 ** 20), (True, 5, 2.0 ** 34),
+                                            (True, 150, 2.0 ** 20), (True, 150, 2.0 ** 34)])
+def test_outliers_leave_the_others_what_is_stated(torch, bf16, T, outlier):
+    """An element far above the rest of its row, without and with a weight: 2^-39 of it may be
+    lost of each of the others."""
+    rng = np.random.default_rng(T)
+    x = rng.normal(0, 1, (T, 640))
+    x[:, 77] = outlier
+    got, want, bound = products(torch, T, 2, 1, T, 140, 640, 32, True, False, bf16, x=x, zero_column=77)
+    within(got, want, bound, "no weight on the outlier")
+    assert np.abs(want).max() < 100 * 640
+    got, want, bound = products(torch, T, 2, 1, T, 140, 640, 32, True, False, bf16, x=x)
+    within(got, want, bound, "a weight on the outlier")
+    if bf16 and outlier < 2.0 ** 30 and T <= 48:   # above 2^-31 of the largest nothing is lost
+        got, want, _ = products(torch, T, 2, 1, T, 140, 640, 32, True, False, bf16, x=x, zero_column=77)
+        assert float((got != num(torch.from_numpy(want).to(torch.bfloat16))).mean()) <= 2 * mb.MISROUNDED
