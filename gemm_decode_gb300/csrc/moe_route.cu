@@ -13,12 +13,13 @@
 // warp is the number of earlier lanes of the match), then sums the counts of the warps
 // before.  With one block (up to 512 choices: decoding) the same launch adds the
 // prefix over the experts and is done; with more, each block writes its histogram and a
-// second launch adds the histograms of the blocks before it.  No atomics: the order is
-// the same on every run.
+// second launch adds the histograms of the blocks before it; with more than kDirect blocks,
+// whose histograms together every block would have to read, a launch between the two sums
+// them once.  No atomics: the order is the same on every run.
 //
 // Bound: latency (the k dependent rounds of one warp, the block barriers, the second launch).
 // Measured: one token, 8 of 64 experts 3.1 us; 8191 tokens, 8 of 128 experts 16.5 us (20.4
-// with blocks of 1024 choices and no logits fetched ahead).
+// with blocks of 1024 choices and no logits fetched ahead); 131072 tokens 135 us.
 #include "q4_moe.cuh"
 
 namespace q4 {
@@ -26,6 +27,10 @@ namespace q4 {
 namespace {
 
 constexpr int kChoices = 512;   // choices (token, place) ranked by one block
+// Blocks up to which each adds the histograms of the others itself (every block reads them
+// all, so the time grows with the square).  8 of 128 experts, without / with the scan: 257
+// blocks 24.0 / 24.9 us, 512 51.8 / 42.3, 2048 320 / 135, 16384 13202 / 1085.
+constexpr int kDirect = 256;
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -124,16 +129,18 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
                     if (v[c] > -INFINITY) s_all += expf(v[c] - m_all);
                 s_all = warp_sum(s_all);
             }
+            if (on_score) {
+#pragma unroll
+                for (int c = 0; c < NV; ++c)   // (an expert whose logit is -inf stays out, whatever its bias)
+                    if (v[c] > -INFINITY)
+                        v[c] = a.sigmoid ? 1.0f / (1.0f + expf(-v[c])) : expf(v[c] - m_all) / s_all;
+            }
             uint32_t key[NV], best = 0;
 #pragma unroll
             for (int c = 0; c < NV; ++c) {
                 const int e = c * 32 + lane;
                 const float b = a.bias != nullptr && e < a.E ? a.bias[e] : 0.0f;
-                float sel = v[c];
-                // (an expert whose logit is -inf stays out, whatever its bias)
-                if (on_score && v[c] > -INFINITY)
-                    sel = a.sigmoid ? 1.0f / (1.0f + expf(-v[c])) : expf(v[c] - m_all) / s_all;
-                key[c] = choice_key(a.bias != nullptr ? sel + b : sel);
+                key[c] = choice_key(a.bias != nullptr ? v[c] + b : v[c]);
                 best = max(best, key[c]);
             }
             for (int j = 0; j < a.k; ++j) {
@@ -207,9 +214,42 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
     }
 }
 
-// The second launch of a long prompt: first row of each expert for this block (all choices
+// Histograms [blocks][E] to exclusive prefixes over the blocks, in place, and the totals of
+// the experts behind them.  A block takes 32 experts, a warp a 32nd of the blocks.
+__global__ void __launch_bounds__(1024) route_scan_kernel(const RouteArgs a, int blocks) {
+    __shared__ int part[32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + lane;
+    const int each = (blocks + 31) / 32, b0 = warp * each, b1 = min(b0 + each, blocks);
+    wait_prior_grid();
+    allow_next_grid();
+    int sum = 0;
+    if (e < a.E) {
+#pragma unroll 8
+        for (int b = b0; b < b1; ++b) sum += a.hist[static_cast<int64_t>(b) * a.E + e];
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += part[w][lane];
+    if (e >= a.E) return;
+    if (warp == 31) a.hist[static_cast<int64_t>(blocks) * a.E + e] = before + sum;
+    for (int b = b0; b < b1; b += 8) {   // eight loads in flight together
+        int h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = b + i < b1 ? a.hist[static_cast<int64_t>(b + i) * a.E + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (b + i < b1) a.hist[static_cast<int64_t>(b + i) * a.E + e] = before;
+            before += h[i];
+        }
+    }
+}
+
+// The last launch of a long prompt: first row of each expert for this block (all choices
 // of lower experts, and this expert's choices in the blocks before), then the rows.
-__global__ void __launch_bounds__(1024) route_place_kernel(const RouteArgs a, int per_block) {
+// scanned: the histograms are prefixes already.
+__global__ void __launch_bounds__(1024) route_place_kernel(const RouteArgs a, int per_block, int scanned) {
     __shared__ int part_all[1024], part_before[1024], base[kMaxExperts], sums[33];
     int width = 32;
     while (width < a.E) width <<= 1;            // <= 1024: threads of one slice of the blocks
@@ -218,7 +258,12 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteArgs a, in
     wait_prior_grid();
     allow_next_grid();
     int all = 0, before = 0;
-    if (e < a.E) {
+    if (scanned) {
+        if (slice == 0 && e < a.E) {
+            all = a.hist[static_cast<int64_t>(gridDim.x) * a.E + e];
+            before = a.hist[static_cast<int64_t>(blockIdx.x) * a.E + e];
+        }
+    } else if (e < a.E) {
 #pragma unroll 8
         for (int b = slice; b < static_cast<int>(gridDim.x); b += slices) {
             const int h = a.hist[static_cast<int64_t>(b) * a.E + e];
@@ -258,11 +303,14 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteArgs a, in
 }
 
 static int route_per_block(int k) { return kChoices / k; }
+static int route_blocks(int T, int k) {
+    const int per = route_per_block(k);
+    return T / per + (T % per != 0);
+}
 
 int64_t route_workspace_bytes(int T, int E, int k) {
-    const int per = route_per_block(k);
-    if (T <= per) return 0;
-    return (static_cast<int64_t>(T) + per - 1) / per * E * 4;
+    const int blocks = route_blocks(T, k);
+    return blocks > 1 ? (static_cast<int64_t>(blocks) + (blocks > kDirect)) * E * 4 : 0;
 }
 
 template <int NV>
@@ -274,7 +322,7 @@ static int launch_choose(const RouteArgs &a, int blocks, int threads, int per, c
 
 int launch_route(const RouteArgs &a, cudaStream_t stream) {
     const int per = route_per_block(a.k);
-    const int blocks = (a.T + per - 1) / per;
+    const int blocks = route_blocks(a.T, a.k);
     // a thread per choice and per expert of the block
     const int choices = blocks > 1 ? kChoices : a.T * a.k, need = choices > a.E ? choices : a.E;
     const int threads = need <= 128 ? 128 : (need + 31) / 32 * 32;
@@ -286,7 +334,11 @@ int launch_route(const RouteArgs &a, cudaStream_t stream) {
     else if (a.E <= 512) st = launch_choose<16>(a, blocks, threads, per, stream);
     else st = launch_choose<32>(a, blocks, threads, per, stream);
     if (st != Q4_OK || blocks == 1) return st;
-    return launch_overlappable(route_place_kernel, dim3(blocks), dim3(1024), 0, stream, true, a, per);
+    const bool scan = blocks > kDirect;
+    if (scan)
+        st = launch_overlappable(route_scan_kernel, dim3((a.E + 31) / 32), dim3(1024), 0, stream, true, a, blocks);
+    if (st != Q4_OK) return st;
+    return launch_overlappable(route_place_kernel, dim3(blocks), dim3(1024), 0, stream, true, a, per, scan ? 1 : 0);
 }
 
 }  // namespace q4

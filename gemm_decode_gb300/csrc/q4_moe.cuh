@@ -19,7 +19,7 @@ struct RouteArgs {
     int *ids;
     float *weights;
     int *offsets, *rows, *pos;
-    int *hist;   // [blocks][E] choices of each block of tokens (several blocks only)
+    int *hist;   // [blocks][E] choices of each block of tokens (several blocks only), [E] totals (many)
 };
 int64_t route_workspace_bytes(int T, int E, int k);
 int launch_route(const RouteArgs &a, cudaStream_t stream);

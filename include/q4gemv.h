@@ -373,7 +373,7 @@ Q4_API int64_t q4moe_route_workspace(int32_t T, int32_t E, int32_t top_k);
  *     ascend; -1 from offsets[E] on
  *   pos : device int32 [T][top_k], the row of each choice, or -1
  * 1 <= E <= 1024, 1 <= top_k <= min(E, 32), T * top_k < 2^31 (Q4_ERR_UNSUPPORTED above
- * the upper limits).  T == 0 is an empty problem. */
+ * the upper limits).  T == 0 is an empty problem: nothing is written. */
 Q4_API int q4moe_route_run(const float *logits, const float *bias_or_null, const uint8_t *token_mask_or_null, int32_t T,
                     int32_t E, int32_t top_k, int32_t score, int32_t renormalize, float scale, int32_t *ids,
                     float *weights, int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace,

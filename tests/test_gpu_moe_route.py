@@ -89,12 +89,11 @@ def test_bias_on_the_score(torch, T, E, k, kind, renorm):
     live = mask != 0
     assert (ids[~live] == -1).all() and (w[~live] == 0).all() and (pos[~live] == -1).all()
     p = scores(logits, kind)
-    with np.errstate(invalid="ignore"):
-        spread = np.nanmax(np.where(np.isfinite(logits), logits, np.nan), axis=1) if kind == "softmax" else np.zeros(T)
-        low = np.where(live, np.nanmin(np.where(np.isfinite(logits), logits, np.nan), axis=1, initial=0.0), 0.0)
+    ok = np.isfinite(logits)
+    spread = np.where(ok, logits, -np.inf).max(axis=1, initial=0.0) - np.where(ok, logits, np.inf).min(axis=1, initial=0.0)
     # a score is off by a few steps of binary32 (expf 2 ulp, E additions, a division), and is
     # rounded once more with the bias added; two sums nearer than that may change places
-    off_by = (E + 20 + 2 * (np.nan_to_num(spread) - low)) * U32 * p.max(axis=1) + 2 * U32 * (1.0 + np.abs(bias).max())
+    off_by = (E + 20 + 2 * spread) * U32 * p.max(axis=1) + 2 * U32 * (1.0 + np.abs(bias).max())
     sel = np.where(np.isneginf(logits) | np.isnan(logits), -np.inf, p + bias.astype(np.float64))
     for t in np.nonzero(live)[0]:
         chosen = ids[t]
@@ -104,7 +103,57 @@ def test_bias_on_the_score(torch, T, E, k, kind, renorm):
         assert np.delete(sel[t], chosen).max() <= got.min() + 2 * off_by[t], "the largest"
     v = np.take_along_axis(p, np.maximum(ids, 0), 1)
     if renorm:
-        v = v / (v.sum(axis=1, keepdims=True) + (1e-20 if kind == "sigmoid" else 0.0))
+        v = v / (v.sum(axis=1, keepdims=True) + (1e-20 if kind == "sigmoid" else 1e-300))
     within(w[live].astype(np.float64), 2.5 * v[live], (E + 60) * U32 * 2.5 * v[live] + 1e-37, "weights")
     for got, e in zip((off, rows, pos), grouped(ids, E)):
         assert np.array_equal(got, e)
+
+
+def long_prompt(torch, T, E, k, seed):
+    """Logits, mask, and the chosen experts by a plain stable sort."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    logits = torch.randn(T, E, device="cuda", generator=g)
+    logits[:, E // 3] += 2.0
+    mask = (torch.rand(T, device="cuda", generator=g) < 0.9).to(torch.uint8)
+    ids = torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :k].to(torch.int32)
+    ids[mask == 0] = -1
+    return logits, mask, ids
+
+
+# blocks of 512 // k tokens: 256 and 257 of them, several thousand, a last one that is not full
+@pytest.mark.parametrize("T,E,k", [(4096, 40, 32), (4097, 40, 32), (80003, 40, 32), (300000, 8, 8), (131071, 1000, 16),
+                                   (270000, 3, 2)])
+def test_order_of_long_prompts(torch, T, E, k):
+    logits, mask, ids = long_prompt(torch, T, E, k, T)
+    i = lambda *s: torch.full(s, 77, dtype=torch.int32, device="cuda")  # noqa: E731
+    got, off, rows, pos = i(T, k), i(E + 1), i(T * k), i(T, k)
+    w = torch.empty(T, k, device="cuda")
+    n = q4.q4moe_route_workspace(T, E, k)
+    ws = work(torch, n + 4096)
+    ws[n:] = 77
+    q4.q4moe_route_run(logits, got, w, off, rows, pos, ws[:n], token_mask=mask)
+    assert torch.equal(got, ids)
+    for have, want in zip((off, rows, pos), grouped(ids.cpu().numpy(), E)):
+        assert np.array_equal(have.cpu().numpy(), want)
+    assert bool((ws[n:] == 77).all())
+
+
+def test_time_grows_with_the_tokens(torch):
+    """Four times the tokens take no more than about four times as long (each block's own sum
+    over all blocks would take sixteen times as long)."""
+    def best(T, E=128, k=8):
+        logits, mask, ids = long_prompt(torch, T, E, k, 1)
+        outs = [torch.empty_like(ids), torch.empty(T, k, device="cuda"), torch.empty(E + 1, dtype=torch.int32, device="cuda"),
+                torch.empty(T * k, dtype=torch.int32, device="cuda"), torch.empty_like(ids),
+                work(torch, q4.q4moe_route_workspace(T, E, k))]
+        times = []
+        for _ in range(8):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            q4.q4moe_route_run(logits, *outs, token_mask=mask)
+            end.record()
+            torch.cuda.synchronize()
+            times.append(start.elapsed_time(end))
+        return min(times[2:])
+    few, many = best(1 << 18), best(1 << 20)
+    assert many <= 8 * few, (few, many)
