@@ -43,7 +43,10 @@ int gemm_shape(int64_t R, int64_t Tx, int64_t E, int64_t N, int64_t K, int32_t g
     if (Tx < 0 || E < 1 || !valid_dtype(dtype)) return Q4_ERR_INVALID_ARG;
     if (epilogue != Q4_EPILOGUE_NONE && epilogue != Q4_EPILOGUE_SWIGLU) return Q4_ERR_INVALID_ARG;
     if (epilogue == Q4_EPILOGUE_SWIGLU && N % 2 != 0) return Q4_ERR_INVALID_ARG;
-    if (E > kMaxExperts || R > 0x7fffffffLL || Tx > 0x7fffffffLL || E * N > 0x7fffffffLL) return Q4_ERR_UNSUPPORTED;
+    if (E > kMaxExperts || R > 0x7fffffffLL || Tx >= 0x7fffffffLL || E * N > 0x7fffffffLL || K > kMaxMoeK)
+        return Q4_ERR_UNSUPPORTED;
+    // the kernels count items in 32 bits; no y that fits a device has as many
+    if (!moe_gemm_countable(R, static_cast<int>(E), N, group, dtype == Q4_BF16)) return Q4_ERR_UNSUPPORTED;
     return Q4_OK;
 }
 

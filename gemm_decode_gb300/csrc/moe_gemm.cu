@@ -91,6 +91,12 @@ int launch_many(const CUtensorMap &codes, const MoeKernelArgs &g, cudaStream_t s
 
 }  // namespace
 
+// Items are counted in 32 bits (and so are units while the K of items is shared).
+bool moe_gemm_countable(int64_t R, int E, int64_t N, int group, bool bf16) {
+    const Tile t = tile_of(R, E, group, bf16);
+    return R / t.nt + std::min<int64_t>(R, E) <= 0x7fffffffLL / ((N + 128 * t.rt - 1) / (128 * t.rt) + 1);
+}
+
 int64_t moe_gemm_workspace_bytes(int64_t R, int64_t Tx, int64_t, int64_t K, int E, bool bf16) {
     int64_t most = 0;   // whatever the group
     for (int group : {32, 64, 128})
@@ -101,9 +107,6 @@ int64_t moe_gemm_workspace_bytes(int64_t R, int64_t Tx, int64_t, int64_t K, int 
 int launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t stream) {
     const bool bf16 = a.bf16 != 0;
     const Tile t = tile_of(a.R, a.E, a.group, bf16);
-    // items are counted in 32 bits, and so are units while the K of items is shared
-    const int64_t most = (a.R / t.nt + std::min<int64_t>(a.R, a.E)) * ((a.N + 128 * t.rt - 1) / (128 * t.rt));
-    if (most > 0x7fffffffLL || a.K > (1 << 26)) return Q4_ERR_UNSUPPORTED;
     const Layout l = layout_of(a.R, a.Tx, a.K, t, bf16);
     unsigned char *w = static_cast<unsigned char *>(a.workspace);
     MoeKernelArgs g;

@@ -9,6 +9,7 @@ namespace q4 {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 constexpr int kMaxNormH = 16384;
+constexpr int64_t kMaxMoeK = 1 << 26;   // units of 128 k are counted in 32 bits
 
 struct RouteArgs {
     const float *logits, *bias;
@@ -37,6 +38,7 @@ struct MoeGemmArgs {
     int bf16, swiglu;
     void *workspace;
 };
+bool moe_gemm_countable(int64_t R, int E, int64_t N, int group, bool bf16);
 int64_t moe_gemm_workspace_bytes(int64_t R, int64_t Tx, int64_t N, int64_t K, int E, bool bf16);
 int launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t stream);
 

@@ -401,7 +401,8 @@ Q4_API int64_t q4moe_gemm_workspace(int64_t R, int64_t Tx, int64_t N, int64_t K,
  * elements more than 2^17 (Q4_F32) or 2^31 (Q4_BF16) below its largest keep only what the
  * absolute term leaves of them.  A row with a NaN or infinity gives non-finite outputs in
  * that row alone.
- * 1 <= E <= 1024, R and Tx < 2^31, E * N < 2^31, K <= 2^26 (Q4_ERR_UNSUPPORTED above). */
+ * 1 <= E <= 1024, R < 2^31, Tx < 2^31 - 1, E * N < 2^31, K <= 2^26 (Q4_ERR_UNSUPPORTED
+ * above). */
 Q4_API int q4moe_gemm_run(const void *codes, const void *scales_f16, const void *zeros_u4_or_null, const void *x,
                    const int32_t *rows_or_null, const int32_t *offsets, void *y, int32_t E, int64_t R, int64_t Tx,
                    int64_t N, int64_t K, int32_t group, int32_t dtype, int32_t epilogue, void *workspace,
