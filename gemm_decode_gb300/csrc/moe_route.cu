@@ -50,6 +50,12 @@ __device__ __forceinline__ uint32_t choice_key(float sel) {
     return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
+// 1 / (1 + exp(-l)) without an exponential that overflows: relative accuracy for any l.
+__device__ __forceinline__ float sigmoid(float l) {
+    const float e = expf(-fabsf(l));
+    return (l < 0.0f ? e : 1.0f) / (1.0f + e);
+}
+
 // Exclusive prefix over v[0..E) held by thread e, E <= blockDim.x; sums: 33 ints of shared
 // memory.  Returns the prefix of thread e; *total receives the sum of all.
 __device__ __forceinline__ int block_prefix(int v, int *sums, int *total) {
@@ -133,7 +139,7 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
 #pragma unroll
                 for (int c = 0; c < NV; ++c)   // (an expert whose logit is -inf stays out, whatever its bias)
                     if (v[c] > -INFINITY)
-                        v[c] = a.sigmoid ? 1.0f / (1.0f + expf(-v[c])) : expf(v[c] - m_all) / s_all;
+                        v[c] = a.sigmoid ? sigmoid(v[c]) : expf(v[c] - m_all) / s_all;
             }
             uint32_t key[NV], best = 0;
 #pragma unroll
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
         float w = 0.0f;
         const float l = mine >= 0 ? a.logits[static_cast<int64_t>(t) * a.E + mine] : -INFINITY;
         if (a.sigmoid) {
-            w = mine >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+            w = mine >= 0 ? sigmoid(l) : 0.0f;
             if (a.renorm) w = w / (warp_sum(w) + 1e-20f);
         } else {
             const float m = a.renorm ? warp_max(l) : m_all;

@@ -157,3 +157,17 @@ def test_time_grows_with_the_tokens(torch):
         return min(times[2:])
     few, many = best(1 << 18), best(1 << 20)
     assert many <= 8 * few, (few, many)
+
+
+@pytest.mark.parametrize("flag", [0, q4.Q4_ROUTE_SCORE_BIAS])
+def test_sigmoids_of_far_logits(torch, flag):
+    """Renormalised sigmoids of logits where exp(-l) overflows: s / (sum s + 1e-20)."""
+    logits = np.array([[-90.0, -91.0, -95.0, -99.0], [-88.0, -100.0, -3.0e4, -95.0], [90.0, -90.0, 200.0, -89.0]], np.float32)
+    ids, w, *_ = run(torch, logits, 3, q4.Q4_ROUTE_SIGMOID | flag, True, bias=np.zeros(4, np.float32) if flag else None)
+    assert ids[:2].tolist() == [[0, 1, 2], [0, 3, 1]] and (ids[2] != 3).sum() >= 2
+    s = 1.0 / (1.0 + np.exp(-np.take_along_axis(logits, ids, 1).astype(np.float64)))
+    want = s / (s.sum(axis=1, keepdims=True) + 1e-20)
+    # binary32's last step, 2^-149, where s is subnormal
+    within(w.astype(np.float64), want, want * (60 * U32 + 2.0 ** -149 / np.maximum(s, 2.0 ** -149)) + 1e-37, "weights")
+    alone = run(torch, logits[:, :1], 1, q4.Q4_ROUTE_SIGMOID | flag, False)[1]
+    within(alone.astype(np.float64), 1.0 / (1.0 + np.exp(-logits[:, :1].astype(np.float64))), 60 * U32 + 0 * alone, "alone")
