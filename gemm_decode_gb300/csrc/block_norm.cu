@@ -88,12 +88,17 @@ __device__ __forceinline__ float block_sum(float v, float *warp_sums) {
 }  // namespace
 
 template <typename T, int V, int NI>
-__global__ void __launch_bounds__(kNormThreads, 2) block_norm_kernel(const q4_block_norm_t g) {
+__global__ void __launch_bounds__(kNormThreads, 2) block_norm_kernel(const q4_block_norm_t g, unsigned int *bounds) {
     __shared__ float sums[64];
     __shared__ float w_s[kMaxTopK];
     __shared__ int pos_s[kMaxTopK];
     const int t = blockIdx.x;
     const int H = g.H;
+    // (bounds-checking builds) columns [c, c + V) of row r of an array of `rows` rows, aligned as accessed
+    auto ib = [&](int64_t r, int64_t rows, int c, const void *p) {
+        return q4_in_bounds(r >= 0 && r < rows && c + V <= H && reinterpret_cast<uintptr_t>(p) % (V * sizeof(T)) == 0,
+                            bounds);
+    };
     const T *y = static_cast<const T *>(g.y);
     const T *x = static_cast<const T *>(g.x) + static_cast<int64_t>(t) * H;
     wait_prior_grid();
@@ -111,9 +116,9 @@ __global__ void __launch_bounds__(kNormThreads, 2) block_norm_kernel(const q4_bl
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c < H) {
+        if (c < H && ib(t, g.T, c, x + c)) {
             xv[i] = load_pack<T, V>(x + c);
-            if (gate != nullptr) gv[i] = load_pack<T, V>(gate + c);
+            if (gate != nullptr && ib(t, g.T, c, gate + c)) gv[i] = load_pack<T, V>(gate + c);
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) b[i][v] = 0.0f;
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) block_norm_kernel(const q4_bl
                     Pack<T, V> in[4] = {};
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        if (row[q] != nullptr) in[q] = load_pack<T, V>(row[q] + c);
+                        if (row[q] != nullptr && ib(pos_s[j0 + q], g.R, c, row[q] + c)) in[q] = load_pack<T, V>(row[q] + c);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) block_norm_kernel(const q4_bl
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * V;
-            if (c < H) {
+            if (c < H && ib(t, g.R, c, y + static_cast<int64_t>(t) * H + c)) {
                 const Pack<T, V> in = load_pack<T, V>(y + static_cast<int64_t>(t) * H + c);
 #pragma unroll
                 for (int v = 0; v < V; ++v) b[i][v] = to_float(in.v[v]);
@@ -184,7 +189,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) block_norm_kernel(const q4_bl
                 b[i][v] = fmaf(g.residual_scale, to_float(xv[i].v[v]), b[i][v]);
                 ss = fmaf(b[i][v], b[i][v], ss);
             }
-            store_pack<T, V>(static_cast<T *>(g.out) + static_cast<int64_t>(t) * H + c, b[i]);
+            T *to = static_cast<T *>(g.out) + static_cast<int64_t>(t) * H + c;
+            if (ib(t, g.T, c, to)) store_pack<T, V>(to, b[i]);
         }
     }
     if (g.pre_gamma == nullptr) return;
@@ -197,7 +203,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) block_norm_kernel(const q4_bl
             load_floats<V>(g.pre_gamma + c, w);
 #pragma unroll
             for (int v = 0; v < V; ++v) b[i][v] = b[i][v] * r * w[v];
-            store_pack<T, V>(static_cast<T *>(g.out_norm) + static_cast<int64_t>(t) * H + c, b[i]);
+            T *to = static_cast<T *>(g.out_norm) + static_cast<int64_t>(t) * H + c;
+            if (ib(t, g.T, c, to)) store_pack<T, V>(to, b[i]);
         }
     }
 }
@@ -208,7 +215,8 @@ static int launch_norm(const q4_block_norm_t &a, cudaStream_t stream) {
     const int vecs = a.H / V;
     auto launch = [&](auto kernel, int ni) {
         const unsigned threads = static_cast<unsigned>(((vecs + ni - 1) / ni + 31) / 32 * 32);
-        return launch_overlappable(kernel, dim3(static_cast<unsigned>(a.T)), dim3(threads), 0, stream, overlap, a);
+        return launch_overlappable(kernel, dim3(static_cast<unsigned>(a.T)), dim3(threads), 0, stream, overlap, a,
+                                   bounds_counter());
     };
     // vectors per thread; H is at most kMaxNormH
     constexpr int kMost = kMaxNormH / V / kNormThreads;

@@ -131,7 +131,8 @@ int q4moe_route_run(const float *logits, const float *bias_or_null, const uint8_
     }
     CallScope scope(co);
     RouteArgs a = {logits, bias_or_null, token_mask_or_null, T, E, top_k, is_sigmoid(score), renormalize != 0,
-                   is_score_bias(score), scale, ids, weights, offsets, rows, pos, static_cast<int *>(workspace)};
+                   is_score_bias(score), scale, ids, weights, offsets, rows, pos, static_cast<int *>(workspace),
+                   bounds_counter()};
     return launch_route(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -268,7 +269,7 @@ int q4moe_block_run(const q4moe_block_t *args, const q4_run_options_t *opts, voi
         *pos = reinterpret_cast<int *>(w + l.pos);
     const RouteArgs r = {g.logits, g.bias_or_null, g.token_mask_or_null, g.T, g.E, g.top_k,
                          is_sigmoid(g.score), g.renormalize != 0, is_score_bias(g.score), g.route_scale, g.ids,
-                         g.route_weights, offsets, rows, pos, reinterpret_cast<int *>(w + l.scratch)};
+                         g.route_weights, offsets, rows, pos, reinterpret_cast<int *>(w + l.scratch), bounds_counter()};
     if ((st = launch_route(r, cs)) != Q4_OK) return st;
     OverlapInside inside;
     const int bf16 = g.dtype == Q4_BF16;

@@ -98,6 +98,8 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
     const int t0 = blockIdx.x * per_block;
     const int tokens = min(per_block, a.T - t0);
     const int choices = tokens * a.k;
+    auto ib = [&](bool ok) { return q4_in_bounds(ok, a.bounds); };   // bounds-checking builds
+    const int64_t all_choices = static_cast<int64_t>(a.T) * a.k;
 
     for (int i = threadIdx.x; i < warps * a.E; i += blockDim.x) count[i] = 0;
     wait_prior_grid();
@@ -108,6 +110,7 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
     auto fetch = [&](int i) {
         if (i >= tokens) return;
         const int t = t0 + i;
+        if (!ib(t >= 0 && t < a.T)) return;
         ahead_live = a.mask == nullptr || a.mask[t] != 0;
         const float *l = a.logits + static_cast<int64_t>(t) * a.E;
 #pragma unroll
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
             w = mine >= 0 && l > -INFINITY ? expf(l - m) : 0.0f;
             w = w / (a.renorm ? warp_sum(w) : s_all);
         }
-        if (lane < a.k) {
+        if (lane < a.k && ib(at + lane < all_choices && i * a.k + lane < kChoices && mine < a.E)) {
             a.ids[at + lane] = mine;
             a.weights[at + lane] = mine >= 0 ? w * a.scale : 0.0f;
             chosen[i * a.k + lane] = mine;
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
     const int e = i < choices ? chosen[i] : -1;
     const unsigned same = __match_any_sync(~0u, e);
     int rank = __popc(same & ((1u << lane) - 1u));
-    if (e >= 0 && rank == 0) count[warp * a.E + e] = static_cast<uint8_t>(__popc(same));
+    if (e >= 0 && rank == 0 && ib(warp < warps && e < a.E)) count[warp * a.E + e] = static_cast<uint8_t>(__popc(same));
     __syncthreads();
     if (e >= 0)
         for (int w = 0; w < warp; ++w) rank += count[w * a.E + e];
@@ -211,12 +214,13 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
         if (i < choices) {
             const int row = e >= 0 ? base[e] + rank : -1;
             a.pos[i] = row;
-            if (row >= 0) a.rows[row] = i / a.k;
-            if (i >= all) a.rows[i] = -1;
+            if (row >= 0 && ib(row < all_choices)) a.rows[row] = i / a.k;
+            if (i >= all && ib(i < all_choices)) a.rows[i] = -1;
         }
     } else {
         if (i < a.E) a.hist[static_cast<int64_t>(blockIdx.x) * a.E + i] = total;
-        if (i < choices) a.pos[static_cast<int64_t>(t0) * a.k + i] = e >= 0 ? rank : -1;
+        if (i < choices && ib(static_cast<int64_t>(t0) * a.k + i < all_choices))
+            a.pos[static_cast<int64_t>(t0) * a.k + i] = e >= 0 ? rank : -1;
     }
 }
 
@@ -299,10 +303,10 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteArgs a, in
     const bool mine = threadIdx.x < per_block * a.k && at < static_cast<int64_t>(a.T) * a.k;
     if (mine) {
         const int id = a.ids[at];
-        if (id >= 0) {
+        if (id >= 0 && q4_in_bounds(id < a.E, a.bounds)) {
             const int row = base[id] + a.pos[at];
             a.pos[at] = row;
-            a.rows[row] = static_cast<int>(at / a.k);
+            if (q4_in_bounds(row >= 0 && row < total, a.bounds)) a.rows[row] = static_cast<int>(at / a.k);
         }
         if (at >= total) a.rows[at] = -1;
     }

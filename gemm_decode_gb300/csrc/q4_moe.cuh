@@ -21,6 +21,7 @@ struct RouteArgs {
     float *weights;
     int *offsets, *rows, *pos;
     int *hist;   // [blocks][E] choices of each block of tokens (several blocks only), [E] totals (many)
+    unsigned int *bounds;   // counter of bounds-checking builds
 };
 int64_t route_workspace_bytes(int T, int E, int k);
 int launch_route(const RouteArgs &a, cudaStream_t stream);
