@@ -31,10 +31,11 @@
 // What bounds it: the warps' instructions and the latency of the hand-overs, not HBM.  Logic
 // and binary16 arithmetic together issue 2.5 warp instructions per clock and SM (measured),
 // so dequantisation alone takes 250 cycles per unit, where HBM would deliver one in 360; with
-// the other roles beside it a unit takes about 730.  Measured: 8 experts of 28672 x 4096
-// (groups of 128), 48 tokens bfloat16: 144 us, 3.4 TB/s (0.50 of measured).  Scaled weights
-// and one sum over K, as in moe_gemm_many.cuh, took 152 us there; one epilogue group for all
-// units 187 us; two MMA warps 160 us.
+// the other roles beside it a unit takes about 730 (from the time below; 826 in a profile of
+// half as many tokens, where dequantisation is 41 % of the instructions).  Measured: 8 experts
+// of 28672 x 4096 (groups of 128), 48 tokens bfloat16: 144 us, 3.4 TB/s (0.50 of measured).
+// Scaled weights and one sum over K, as in moe_gemm_many.cuh, took 152 us there; one epilogue
+// group for all units 187 us; two MMA warps 160 us.
 #pragma once
 
 #include "moe_gemm_common.cuh"
@@ -164,7 +165,7 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
         fail();
         return false;
     };
-    uint32_t units_issued = 0;   // warp 1: units whose MMAs were issued
+    uint32_t units_issued = 0;   // warp 0 (lane 0): units whose codes are copied; warp 1: whose MMAs were issued
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegMisc));
@@ -172,7 +173,6 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
             // -------------------------------------------------------- codes
             if (lane == 0) {
                 Ring<S::kCodeStages> r;
-                uint32_t issued = 0;
                 MoeSegment s = {};
                 bool ok = true;
                 while (ok && next_segment<NT>(plan, s)) {
@@ -186,15 +186,19 @@ moe_gemm_few_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKern
                         tma_load_2d(smem_addr(code_ring + r.s * S::kCodeBytes), &map_codes, code_full(r.s),
                                     u * (kUnit / 2), row);
                         r.step();
-                        ++issued;
+                        ++units_issued;
                     }
                 }
-                // Every copy lands before the CTA may exit, whichever role gives up, and when: a
-                // flag read here could be raised a moment later.  (Otherwise the copies are
-                // waited for anyway, by the dequantisers.)
-                for (uint32_t j = issued > S::kCodeStages ? issued - S::kCodeStages : 0; j < issued; ++j)
-                    mbar_wait(code_full(static_cast<int>(j % S::kCodeStages)), (j / S::kCodeStages) & 1u,
-                              50ull * 1000 * 1000);
+            }
+            __syncwarp();
+            // Every copy lands before the CTA may exit, whichever role gives up, and when: a flag
+            // read here could be raised a moment later.  (Otherwise the copies are waited for
+            // anyway, by the dequantisers.)  A lane per stage: one lane for all of them took
+            // 0.8 us longer on 1024 binary32 tokens (112 us), behind the last barrier 2 us.
+            const uint32_t copied = __shfl_sync(~0u, units_issued, 0);
+            if (lane < S::kCodeStages && static_cast<uint32_t>(lane) < copied) {
+                const uint32_t j = copied - 1 - lane;
+                mbar_wait(code_full(static_cast<int>(j % S::kCodeStages)), (j / S::kCodeStages) & 1u, 50ull * 1000 * 1000);
             }
         } else if (warp == 1) {
             // -------------------------------------------------------- MMA

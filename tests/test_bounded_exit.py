@@ -12,7 +12,6 @@ import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gemm_decode_gb300", "csrc")
 FLAG = r"if \((?:\*abort_flag|aborted\(\))\)"
-COMMENT = r"(?:\s|//[^\n]*\n)*"
 
 
 def source(name):
@@ -24,9 +23,11 @@ def source(name):
                                   "q4gemv_tc.cu", "q4gemv_stream_kernel.cuh"])
 def test_copies_are_drained_whatever_the_flag(name):
     text = source(name)
-    drain = re.search(r"for \([^;]*issued[^;]*;[^;]*issued; \+\+\w+\)" + COMMENT + r"mbar_wait\(", text)
-    assert drain, "the copying lane waits for the copies it issued"
-    assert not re.search(FLAG + COMMENT + r"\{?" + COMMENT + r"for \([^;]*issued", text), "the drain depends on a flag"
+    drains = list(re.finditer(r"mbar_wait\((?:code_full|full_a|cfull|full)\([^;]*50ull \* 1000 \* 1000\);", text))
+    assert len(drains) == 1, "the copying warp waits for the copies it issued"
+    before = text[:drains[0].start()]
+    last_copy = max(before.rfind("tma_load_2d("), before.rfind("bulk_copy("))
+    assert last_copy > 0 and not re.search(FLAG, before[last_copy:]), "the drain depends on a flag"
 
 
 @pytest.mark.parametrize("name", ["q4gemm.cu", "q4gemm_split.cu", "q4gemv_tc.cu"])
