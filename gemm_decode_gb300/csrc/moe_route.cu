@@ -1,8 +1,8 @@
 // moe_route.cu -- the router of a mixture of experts: each token's top-k experts with
 // their weights, and the rows grouped by expert.
 //
-// A warp owns a token.  Its E logits sit in registers (E / 32 per lane); each becomes a
-// 32-bit key that orders as the binary32 value does (0: never chosen), so a round of the
+// A warp owns a token.  Its E logits sit in registers (E / 32 per lane; above 256 experts
+// some are spilled); each becomes a 32-bit key that orders as the binary32 value does (0: never chosen), so a round of the
 // choice is one integer maximum over the warp and one minimum over the indices that hold
 // it -- exact, with ties to the lower expert, and without a floating-point comparison of
 // rounded scores: softmax and sigmoid rise with the logit, so the choice needs them only
@@ -17,7 +17,8 @@
 // whose histograms together every block would have to read, a launch between the two sums
 // them once.  No atomics: the order is the same on every run.
 //
-// Bound: latency (the k dependent rounds of one warp, the block barriers, the second launch).
+// Bound: latency (the k dependent rounds of one warp, the block barriers, the later launches);
+// with up to kDirect blocks also the histograms, which each of them reads.
 // Measured: one token, 8 of 64 experts 3.1 us; 8191 tokens, 8 of 128 experts 16.5 us (20.4
 // with blocks of 1024 choices and no logits fetched ahead); 131072 tokens 135 us.
 #include "q4_moe.cuh"
@@ -86,8 +87,9 @@ __device__ __forceinline__ int block_prefix(int v, int *sums, int *total) {
 
 }  // namespace
 
-// One block: the choices of tokens [blockIdx.x * per_block, ...).  NV: logits per lane.
-template <int NV>
+// One block: the choices of tokens [blockIdx.x * per_block, ...).  NV: logits per lane;
+// ON_SCORE: the choice is by score + bias.
+template <int NV, bool ON_SCORE>
 __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteArgs a, int per_block, int single) {
     extern __shared__ unsigned char route_smem[];
     int *chosen = reinterpret_cast<int *>(route_smem);                     // [kChoices]
@@ -128,8 +130,7 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
         int mine = -1;   // lane j: the token's j-th choice
         float m_all = -INFINITY, s_all = 0.0f;
         if (live) {
-            const bool on_score = a.score_bias != 0 && a.bias != nullptr;
-            if (!a.sigmoid && (!a.renorm || on_score)) {
+            if (!a.sigmoid && (!a.renorm || ON_SCORE)) {
 #pragma unroll
                 for (int c = 0; c < NV; ++c) m_all = fmaxf(m_all, v[c]);
                 m_all = warp_max(m_all);
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kMaxExperts) route_choose_kernel(const RouteAr
                     if (v[c] > -INFINITY) s_all += expf(v[c] - m_all);
                 s_all = warp_sum(s_all);
             }
-            if (on_score) {
+            if constexpr (ON_SCORE) {
 #pragma unroll
                 for (int c = 0; c < NV; ++c)   // (an expert whose logit is -inf stays out, whatever its bias)
                     if (v[c] > -INFINITY)
@@ -326,8 +327,9 @@ int64_t route_workspace_bytes(int T, int E, int k) {
 template <int NV>
 static int launch_choose(const RouteArgs &a, int blocks, int threads, int per, cudaStream_t stream) {
     const size_t smem = 4 * (kChoices + a.E + 33) + static_cast<size_t>(threads / 32) * a.E;
-    return launch_overlappable(route_choose_kernel<NV>, dim3(blocks), dim3(threads), smem, stream,
-                               call_options().overlap, a, per, blocks == 1 ? 1 : 0);
+    return launch_overlappable(a.score_bias && a.bias != nullptr ? route_choose_kernel<NV, true> : route_choose_kernel<NV, false>,
+                               dim3(blocks), dim3(threads), smem, stream, call_options().overlap, a, per,
+                               blocks == 1 ? 1 : 0);
 }
 
 int launch_route(const RouteArgs &a, cudaStream_t stream) {
