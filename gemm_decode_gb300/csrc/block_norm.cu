@@ -6,7 +6,8 @@
 //   a = x' / sqrt(mean x'^2 + eps) * pre
 //
 // One CTA per token; each thread keeps its NI vectors of the row in registers from the
-// first load to the last store, so every array is read or written once and the two means
+// first load to the last store (beyond 8192 features, 4096 with accesses of two elements or
+// 2048 of one, part of them is spilled), so every array is read or written once and the two means
 // are block sums of registers (binary32, in a fixed order: warps by shuffles, then the
 // warps' sums by every thread).  Loads are up to 16 bytes per thread, four of
 // the token's rows of y at a time in flight together, and those of x and the gate before
@@ -222,7 +223,8 @@ static int launch_norm(const q4_block_norm_t &a, cudaStream_t stream) {
     constexpr int kMost = kMaxNormH / V / kNormThreads;
     if (vecs <= kNormThreads) return launch(block_norm_kernel<T, V, 1>, 1);
     if (vecs <= 2 * kNormThreads) return launch(block_norm_kernel<T, V, 2>, 2);
-    if (vecs <= 4 * kNormThreads) return launch(block_norm_kernel<T, V, 4>, 4);
+    if constexpr (kMost > 4)
+        if (vecs <= 4 * kNormThreads) return launch(block_norm_kernel<T, V, 4>, 4);
     return launch(block_norm_kernel<T, V, kMost>, kMost);
 }
 

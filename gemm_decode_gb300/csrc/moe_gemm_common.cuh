@@ -297,7 +297,9 @@ __device__ __forceinline__ MoePlan make_plan(const MoeKernelArgs &g, const int *
         // whole items when sharing their units would save no more time than joining the parts
         // takes (always from sixteen waves on, so items * units below fits 32 bits).  With
         // kJoin = 7 / 14 / 28: a block of 2048 tokens 231 / 211 / 203 us, one of 8 tokens 85 /
-        // 79 / 81 us, 1024 binary32 tokens 116 / 112 / 112 us, the other sizes alike
+        // 79 / 81 us, 1024 binary32 tokens 116 / 112 / 112 us, the other sizes alike.  One
+        // number, whatever the parts hold (512 bytes to 128 KB per CTA): where they are small
+        // it keeps SMs idle that a cheaper join would use
         plan.whole = plan.items > 0 && (waves >= 16 || static_cast<uint64_t>(waves) * ctas * plan.units <=
                                                            static_cast<uint64_t>(plan.items) * plan.units + kJoin * ctas);
         if (plan.whole) {

@@ -20,9 +20,9 @@
 //                in turn: a thread owns a weight row, reads 64 bytes of codes and writes 128
 //                weights into 64 columns of tensor memory
 //
-// What bounds it: the tensor core is busy 1024 of about 2400 cycles per unit; the rest is the
-// issuing warp's own steps between runs of MMAs, and 0.17 of the time the wait for the
-// epilogue at an item's end.  Measured: 4096 tokens, 8 of 64 experts of 2048 x 2048 (groups
+// What bounds it: the hand-overs between the roles.  The tensor core is busy 930 of 2160
+// cycles per unit (43 %, ncu; 1024 were all 128 rows in use); in the rest the issuing warp
+// waits for weights, for rows of x or, at an item's end, for the epilogue.  Measured: 4096 tokens, 8 of 64 experts of 2048 x 2048 (groups
 // of 64, SwiGLU): 302 us, 911 TFLOP/s (0.48 of measured bf16).  A fourth dequantiser group
 // (310 us) and an MMA warp per weight tile (323 us, with registers spilled) gained nothing.
 #pragma once
@@ -490,7 +490,7 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
             const uint32_t jobs = static_cast<uint32_t>(s.k1 - s.k0) * RT;
             const int first_chunk = s.k0 >> chunk_shift;
             for (; next - before < jobs; next += G) {
-                const int t = RT == 1 ? 0 : static_cast<int>((next - before) % RT);
+                const int t = static_cast<int>((next - before) % RT);
                 const int u = s.k0 + static_cast<int>((next - before) / RT);
                 // the chunk of scales: every group passes through every chunk
                 const uint32_t want = chunk + static_cast<uint32_t>((u >> chunk_shift) - first_chunk) + 1;
@@ -500,7 +500,7 @@ moe_gemm_many_kernel(const __grid_constant__ CUtensorMap map_codes, const MoeKer
                 rc.step(static_cast<int>(unit - unit_at));
                 unit_at = unit;
                 const int slot = ra.s;
-                if (!wait(a_empty(slot), ra.ph ^ 1u)) ok = false;   // before code_full: see MoeShape
+                if (!wait(a_empty(slot), ra.ph ^ 1u)) ok = false;   // before code_full: see ManyShape
                 if (!wait(code_full(rc.s), rc.ph)) ok = false;
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
