@@ -3,7 +3,9 @@
 The functions here carry the C ABI's names (include/q4gemv.h) and only
 marshal arguments: torch tensors (or raw integer device addresses) become
 pointers, sizes are read off the tensors when not given, and the current
-torch CUDA stream is passed unless another is named.  Every step of the
+torch CUDA stream is passed unless another is named.  (The mixture-of-experts
+calls take tensors only, whose types and shapes they check; a program with raw
+addresses calls the C ABI through lib().)  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback of any
 kind -- if the shared library is missing or fails to load, every call raises.
 """

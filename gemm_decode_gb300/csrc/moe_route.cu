@@ -2,11 +2,11 @@
 // their weights, and the rows grouped by expert.
 //
 // A warp owns a token.  Its E logits sit in registers (E / 32 per lane; above 256 experts
-// some are spilled); each becomes a 32-bit key that orders as the binary32 value does (0: never chosen), so a round of the
-// choice is one integer maximum over the warp and one minimum over the indices that hold
-// it -- exact, with ties to the lower expert, and without a floating-point comparison of
-// rounded scores: softmax and sigmoid rise with the logit, so the choice needs them only
-// where a bias is added to the score itself.
+// some are spilled); each becomes a 32-bit key that orders as the binary32 value does (0:
+// never chosen), so a round of the choice is one integer maximum over the warp and one
+// minimum over the indices that hold it -- exact, with ties to the lower expert, and without
+// a floating-point comparison of rounded scores: softmax and sigmoid rise with the logit, so
+// the choice needs them only where a bias is added to the score itself.
 //
 // The grouped order is a counting sort that keeps the order of the tokens.  A block of
 // 512 choices counts them per warp with one match over the warp (the rank inside the
