@@ -4,8 +4,9 @@ The functions here carry the C ABI's names (include/q4gemv.h) and only
 marshal arguments: torch tensors (or raw integer device addresses) become
 pointers, sizes are read off the tensors when not given, and the current
 torch CUDA stream is passed unless another is named.  (The mixture-of-experts
-calls take tensors only, whose types and shapes they check; a program with raw
-addresses calls the C ABI through lib().)  Every step of the
+calls and those for several continuations of one prompt take tensors only,
+whose types and shapes they check; a program with raw addresses calls the C ABI
+through lib().)  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback of any
 kind -- if the shared library is missing or fails to load, every call raises.
 """
@@ -27,6 +28,9 @@ __all__ = [
     "q4gemv_bounds_violations", "q4gemv_grouped_split",
     "q4moe_route_run", "q4moe_route_workspace", "q4moe_gemm_run", "q4moe_gemm_workspace",
     "q4_block_norm_run", "q4moe_block_run", "q4moe_block_workspace",
+    "q4_rope_append_run", "q4_rope_frequencies", "q4_prefix_attn_run", "q4_prefix_attn_workspace",
+    "q4_beam_step_run", "q4_beam_step_workspace", "q4_beam_reorder_run",
+    "Q4_F16", "Q4_ROPE_HALF", "Q4_ROPE_INTERLEAVED", "Q4_ROPE_PLAIN", "Q4_ROPE_LINEAR", "Q4_ROPE_BANDS",
     "Q4_F32", "Q4_BF16", "Q4_ROUTE_SOFTMAX", "Q4_ROUTE_SIGMOID", "Q4_ROUTE_SCORE_BIAS",
     "Q4_OK", "Q4_ERR_INVALID_ARG", "Q4_ERR_UNSUPPORTED", "Q4_ERR_MISALIGNED",
     "Q4_ERR_CUDA", "Q4_ERR_TIMEOUT", "Q4_EPILOGUE_NONE", "Q4_EPILOGUE_SWIGLU",
@@ -40,8 +44,10 @@ HEADER = os.path.join(_ROOT, "include", "q4gemv.h")
 Q4_OK, Q4_ERR_INVALID_ARG, Q4_ERR_UNSUPPORTED, Q4_ERR_MISALIGNED, Q4_ERR_CUDA, Q4_ERR_TIMEOUT = range(6)
 Q4_EPILOGUE_NONE, Q4_EPILOGUE_SWIGLU = 0, 1
 Q4_RUN_OVERLAPPED, Q4_RUN_EXACT_X, Q4_RUN_WAIT_TIMEOUT = 0x1, 0x2, 0x4
-Q4_F32, Q4_BF16 = 0, 1
+Q4_F32, Q4_BF16, Q4_F16 = 0, 1, 2
 Q4_ROUTE_SOFTMAX, Q4_ROUTE_SIGMOID, Q4_ROUTE_SCORE_BIAS = 0, 1, 0x10
+Q4_ROPE_HALF, Q4_ROPE_INTERLEAVED = 0, 1
+Q4_ROPE_PLAIN, Q4_ROPE_LINEAR, Q4_ROPE_BANDS = 0, 1, 2
 
 
 def library_path() -> str:
@@ -94,6 +100,39 @@ class _MoeBlock(ctypes.Structure):
                 [(n, ctypes.c_void_p) for n in ("pre_gamma", "ids", "route_weights", "out", "out_norm",
                                                 "workspace")] +
                 [("workspace_bytes", ctypes.c_int64)])
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("page", ctypes.c_int32), ("pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
+class _RopeAppend(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "Hq", "dtype", "rot", "layout")] +
+                [("scale", ctypes.c_float), ("eps", ctypes.c_float)] +
+                [(n, ctypes.c_void_p) for n in ("q", "k", "v")] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")] +
+                [(n, ctypes.c_void_p) for n in ("q_gamma", "k_gamma", "positions", "inv_freq", "slots", "q_out")] +
+                [("cache", _KvCache)])
+
+
+class _PrefixAttn(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("S", "Hq", "groups", "out_dtype", "max_shared_pages",
+                                               "max_own_pages")] +
+                [("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                 ("cache", _KvCache)] +
+                [(n, ctypes.c_void_p) for n in ("group_offsets", "shared_pages", "shared_lens", "limits", "own_pages",
+                                                "own_lens", "out", "lse", "workspace")] +
+                [("workspace_bytes", ctypes.c_int64)])
+
+
+class _BeamReorder(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("groups", "W", "max_pages", "planes", "heads", "page")] +
+                [(n, ctypes.c_int64) for n in ("pages", "row_bytes", "plane_stride", "page_stride", "head_stride",
+                                               "row_stride")] +
+                [(n, ctypes.c_void_p) for n in ("pool", "tables", "lens", "parents", "spare", "out_tables",
+                                                "out_spare")])
 
 
 _lock = threading.Lock()
@@ -152,7 +191,19 @@ def lib() -> ctypes.CDLL:
                                          _i32, _vp, _i64, _opt, _vp]
             L.q4_block_norm_run.argtypes = [ctypes.POINTER(_BlockNorm), _opt, _vp]
             L.q4moe_block_run.argtypes = [ctypes.POINTER(_MoeBlock), _opt, _vp]
-            for f in ("q4moe_route_run", "q4moe_gemm_run", "q4_block_norm_run", "q4moe_block_run",
+            L.q4_rope_append_run.argtypes = [ctypes.POINTER(_RopeAppend), _opt, _vp]
+            _f64 = ctypes.c_double
+            L.q4_rope_frequencies.argtypes = [ctypes.POINTER(ctypes.c_float), _i32, _f64, _i32, _f64, _f64, _f64, _f64]
+            L.q4_prefix_attn_workspace.argtypes = [_i32] * 5
+            L.q4_prefix_attn_run.argtypes = [ctypes.POINTER(_PrefixAttn), _opt, _vp]
+            L.q4_beam_step_workspace.argtypes = [_i32, _i32, _i32, _i64]
+            L.q4_beam_step_run.argtypes = [_vp, _i64, _vp, _vp, _i32, _i32, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp,
+                                           _i64, _opt, _vp]
+            L.q4_beam_reorder_run.argtypes = [ctypes.POINTER(_BeamReorder), _opt, _vp]
+            for f in ("q4_prefix_attn_workspace", "q4_beam_step_workspace"):
+                getattr(L, f).restype = _i64
+            for f in ("q4_rope_append_run", "q4_rope_frequencies", "q4_prefix_attn_run", "q4_beam_step_run",
+                      "q4_beam_reorder_run", "q4moe_route_run", "q4moe_gemm_run", "q4_block_norm_run", "q4moe_block_run",
                       "q4gemv_pack_info", "q4gemv_run", "q4gemv_fused_run", "q4gemv_grouped_run", "q4_0_gemv_run",
                       "q8_0_gemv_run",
                       "q4gemm_run", "f32gemv_run", "q4gemv_run_ex", "q4gemv_fused_run_ex", "q4gemv_grouped_run_ex",
@@ -458,12 +509,13 @@ def vec4_read_probe_run(buf, nbytes, partial, blocks=0, stream=None, check=True)
 
 class _Types:
     """The torch types of the arrays (looked up once)."""
-    f32 = bf16 = i32 = None
+    f32 = bf16 = i32 = f16 = u8 = None
 
     @classmethod
     def load(cls):
         import torch
         cls.f32, cls.bf16, cls.i32 = torch.float32, torch.bfloat16, torch.int32
+        cls.f16, cls.u8 = torch.float16, torch.uint8
 
 
 def _dtype(t):
@@ -641,4 +693,200 @@ def q4moe_block_run(up, down, logits, a, x, out, out_norm, ids, route_weights, w
     st = lib().q4moe_block_run(ctypes.byref(g), _options(flags, wait_timeout_ns), _stream(stream))
     if check:
         _check(st, "q4moe_block_run")
+    return st
+
+
+# ------------------------------------------------- several continuations of one prompt
+
+def _on(dev, t, name, dtype):
+    """Address of a contiguous tensor of the given type on device `dev` (None passes through)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is required (got strides {tuple(t.stride())})")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: a tensor on CUDA device {dev} expected, got {t.device}")
+    return t.data_ptr()
+
+
+def _device(t, name):
+    """The CUDA device of the call's first tensor, which has to be the current one."""
+    if _Types.f32 is None:
+        _Types.load()
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: a CUDA tensor expected, got {t.device}")
+    import torch
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name}: on CUDA device {dev}, which is not the current one")
+    return dev
+
+
+def _half_dtype(t, name):
+    """Q4_BF16 or Q4_F16 of a tensor."""
+    if t.dtype is _Types.bf16:
+        return Q4_BF16
+    if t.dtype is _Types.f16:
+        return Q4_F16
+    raise ValueError(f"{name}: bfloat16 or float16 expected, got {t.dtype}")
+
+
+def _cache(dev, k, v):
+    """The paged cache of two pools [pages, kv heads, tokens of a page, features]."""
+    pages, heads, page, D = k.shape
+    stride = k.stride()
+    _need(k.shape == v.shape and stride == v.stride() and k.dtype is v.dtype and stride[3] == 1 and
+          k.get_device() == dev and v.get_device() == dev,
+          "k_cache, v_cache: the same shape, strides, type and device, and features side by side")
+    return _KvCache(k.data_ptr(), v.data_ptr(), _half_dtype(k, "k_cache"), heads, D, page, pages, stride[0], stride[1],
+                    stride[2])
+
+
+def _heads(dev, t, name, T, D, dtype):
+    """(address, elements from one token to the next) of [T, heads, D] with the heads of a token side by side."""
+    s, n = t.stride(), t.shape
+    _need(len(n) == 3 and n[0] == T and n[2] == D and (s[2] == 1 or D == 1) and (s[1] == D or n[1] == 1) and
+          t.dtype is dtype and t.get_device() == dev,
+          f"{name}: [tokens, heads, {D}] of {dtype} with the heads of a token side by side expected")
+    return t.data_ptr(), s[0]
+
+
+def q4_rope_append_run(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slots=None, q_gamma=None, k_gamma=None,
+                       eps=1e-6, layout=Q4_ROPE_HALF, scale=1.0, flags=None, stream=None, check=True) -> int:
+    """Norm and rotary positions of q [T, Hq, D] into q_out, and of k [T, Hkv, D] into the
+    cache, with v, at slots [T] (None: token t at slot t).  The heads of a token lie side by
+    side; tokens may be any stride apart, so q, k and v may be parts of one product's rows.
+    k and v None: queries only (k_cache, v_cache None too).  inv_freq [rot / 2] float32:
+    2 len(inv_freq) features are rotated."""
+    dev = _device(q, "q")
+    T, Hq, D = q.shape
+    _need((k is None) == (v is None) and (k is None) == (k_cache is None) and (k is None) == (v_cache is None),
+          "q4_rope_append_run: k, v and the caches come together")
+    if k is not None:
+        cache = _cache(dev, k_cache, v_cache)
+        _need(cache.D == D and k.shape[1] == cache.heads and v.shape == k.shape and
+              q_out.dtype is k_cache.dtype, "q4_rope_append_run: shapes or types do not agree")
+    else:
+        cache = _KvCache(None, None, _half_dtype(q_out, "q_out"), 1, D, 1, 0, 0, 0, 0)
+    _need(q_out.shape == q.shape and (positions is None or positions.numel() == T) and
+          (slots is None or slots.numel() == T) and (q_gamma is None or q_gamma.numel() == D) and
+          (k_gamma is None or k_gamma.numel() == D), "q4_rope_append_run: shapes do not agree")
+    d = _dtype(q)
+    qa, qs = _heads(dev, q, "q", T, D, q.dtype)
+    ka, ks = _heads(dev, k, "k", T, D, q.dtype) if k is not None else (None, 0)
+    va, vs = _heads(dev, v, "v", T, D, q.dtype) if k is not None else (None, 0)
+    a = _RopeAppend(T, Hq, d, 2 * inv_freq.numel() if inv_freq is not None else 0, layout, scale, eps, qa, ka, va,
+                    qs, ks, vs, _on(dev, q_gamma, "q_gamma", _Types.f32), _on(dev, k_gamma, "k_gamma", _Types.f32),
+                    _on(dev, positions, "positions", _Types.i32), _on(dev, inv_freq, "inv_freq", _Types.f32),
+                    _on(dev, slots, "slots", _Types.i32), _on(dev, q_out, "q_out", q_out.dtype), cache)
+    st = lib().q4_rope_append_run(ctypes.byref(a), _options(flags, None), _stream(stream))
+    if check:
+        _check(st, "q4_rope_append_run")
+    return st
+
+
+def q4_rope_frequencies(rot, base=10000.0, kind=Q4_ROPE_PLAIN, factor=1.0, trained=0.0, low=1.0, high=4.0):
+    """Inverse frequencies [rot / 2] (a float32 tensor on the CPU) of rot rotated features,
+    stretched by `factor` for contexts longer than the `trained` tokens."""
+    import torch
+    out = torch.empty(max(0, int(rot)) // 2, dtype=torch.float32)
+    at = ctypes.cast(out.data_ptr() if out.numel() else (ctypes.c_float * 1)(), ctypes.POINTER(ctypes.c_float))
+    _check(lib().q4_rope_frequencies(at, int(rot), float(base), int(kind), float(factor), float(trained), float(low),
+                                     float(high)), "q4_rope_frequencies")
+    return out
+
+
+def q4_prefix_attn_workspace(S, groups, Hq, Hkv, D) -> int:
+    """Bytes of workspace q4_prefix_attn_run needs on the current device."""
+    return _workspace(lib().q4_prefix_attn_workspace(int(S), int(groups), int(Hq), int(Hkv), int(D)),
+                      "q4_prefix_attn_workspace")
+
+
+def q4_prefix_attn_run(q, k_cache, v_cache, out, workspace, group_offsets=None, shared_pages=None, shared_lens=None,
+                       limits=None, own_pages=None, own_lens=None, scale=None, lse=None, flags=None,
+                       wait_timeout_ns=None, stream=None, check=True) -> int:
+    """Attention of q [S, Hq, D] over the segment a group of queries shares (shared_lens
+    [groups], shared_pages [groups, pages], queries group_offsets[g] to group_offsets[g + 1];
+    limits [S]: how much of it each query sees), then each query's own (own_lens [S],
+    own_pages [S, pages]).  scale None: 1 / sqrt(D).  out [S, Hq, D], lse [S, Hq] float32."""
+    dev = _device(q, "q")
+    S, Hq, D = q.shape
+    cache = _cache(dev, k_cache, v_cache)
+    groups = shared_lens.numel() if shared_lens is not None else 0
+    _need((shared_lens is None) == (shared_pages is None) and (own_lens is None) == (own_pages is None) and
+          cache.D == D and out.shape == q.shape and
+          (groups == 0 or (shared_pages.dim() == 2 and shared_pages.shape[0] == groups and
+                           (group_offsets is None or group_offsets.numel() == groups + 1))) and
+          (own_lens is None or (own_pages.dim() == 2 and own_pages.shape[0] == S and own_lens.numel() == S)) and
+          (limits is None or limits.numel() == S) and (lse is None or lse.shape == (S, Hq)),
+          "q4_prefix_attn_run: shapes do not agree")
+    qa, qs = _heads(dev, q, "q", S, D, k_cache.dtype)
+    i32 = _Types.i32
+    out_dtype = Q4_F32 if out.dtype is _Types.f32 else _half_dtype(out, "out")
+    a = _PrefixAttn(S, Hq, groups, out_dtype, shared_pages.shape[1] if groups else 0,
+                    own_pages.shape[1] if own_pages is not None else 0, D ** -0.5 if scale is None else scale, qa, qs,
+                    cache, _on(dev, group_offsets, "group_offsets", i32), _on(dev, shared_pages, "shared_pages", i32),
+                    _on(dev, shared_lens, "shared_lens", i32), _on(dev, limits, "limits", i32),
+                    _on(dev, own_pages, "own_pages", i32), _on(dev, own_lens, "own_lens", i32),
+                    _on(dev, out, "out", out.dtype), _on(dev, lse, "lse", _Types.f32),
+                    _on(dev, workspace, "workspace", _Types.u8), workspace.numel())
+    st = lib().q4_prefix_attn_run(ctypes.byref(a), _options(flags, wait_timeout_ns), _stream(stream))
+    if check:
+        _check(st, "q4_prefix_attn_run")
+    return st
+
+
+def q4_beam_step_workspace(groups, W, K, V) -> int:
+    """Bytes of workspace q4_beam_step_run needs."""
+    return _workspace(lib().q4_beam_step_workspace(int(groups), int(W), int(K), int(V)), "q4_beam_step_workspace")
+
+
+def q4_beam_step_run(logits, scores, tokens, parents, out_scores, workspace, finished=None, out_finished=None, eos=-1,
+                     flags=None, stream=None, check=True) -> int:
+    """The K best continuations of each group: tokens, parents, out_scores (and out_finished,
+    uint8) [groups, K] from logits [groups * W, V] (rows may be any stride apart) and the
+    beams' scores (and finished, uint8) [groups, W]."""
+    dev = _device(logits, "logits")
+    rows, V = logits.shape
+    groups, W = scores.shape
+    of = tokens.shape
+    stride = logits.stride()
+    _need(rows == groups * W and len(of) == 2 and of[0] == groups and parents.shape == of and
+          out_scores.shape == of and (finished is None or finished.shape == scores.shape) and
+          (out_finished is None or out_finished.shape == of) and logits.dtype is _Types.f32 and stride[1] == 1,
+          "q4_beam_step_run: shapes or types do not agree")
+    i32, f32, u8 = _Types.i32, _Types.f32, _Types.u8
+    st = lib().q4_beam_step_run(logits.data_ptr(), stride[0], _on(dev, scores, "scores", f32),
+                                _on(dev, finished, "finished", u8), groups, W, of[1], V, eos,
+                                _on(dev, tokens, "tokens", i32), _on(dev, parents, "parents", i32),
+                                _on(dev, out_scores, "out_scores", f32), _on(dev, out_finished, "out_finished", u8),
+                                _on(dev, workspace, "workspace", u8), workspace.numel(), _options(flags, None),
+                                _stream(stream))
+    if check:
+        _check(st, "q4_beam_step_run")
+    return st
+
+
+def q4_beam_reorder_run(tables, lens, parents, spare, out_tables, out_spare, pool, flags=None, stream=None,
+                        check=True) -> int:
+    """Page tables [groups * W, pages] and the unfinished pages of every plane of pool
+    [planes, pages, heads, tokens of a page, features] follow parents [groups, W]; lens
+    [groups], spare [groups * W]."""
+    dev = _device(pool, "pool")
+    groups, W = parents.shape
+    planes, pages, heads, page, D = pool.shape
+    n, most = tables.shape
+    stride = pool.stride()
+    _need(n == groups * W and lens.numel() == groups and spare.numel() == n and out_spare.numel() == n and
+          out_tables.shape == tables.shape and stride[4] == 1, "q4_beam_reorder_run: shapes do not agree")
+    i32, e = _Types.i32, pool.element_size()
+    a = _BeamReorder(groups, W, most, planes, heads, page, pages, D * e, stride[0] * e, stride[1] * e, stride[2] * e,
+                     stride[3] * e, pool.data_ptr(), _on(dev, tables, "tables", i32), _on(dev, lens, "lens", i32),
+                     _on(dev, parents, "parents", i32), _on(dev, spare, "spare", i32),
+                     _on(dev, out_tables, "out_tables", i32), _on(dev, out_spare, "out_spare", i32))
+    st = lib().q4_beam_reorder_run(ctypes.byref(a), _options(flags, None), _stream(stream))
+    if check:
+        _check(st, "q4_beam_reorder_run")
     return st

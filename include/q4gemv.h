@@ -471,6 +471,195 @@ Q4_API int64_t q4moe_block_workspace(int32_t T, int32_t E, int32_t top_k, int32_
  * overlapped among themselves. */
 Q4_API int q4moe_block_run(const q4moe_block_t *args, const q4_run_options_t *opts, void *stream);
 
+/* ---- several continuations of one prompt --------------------------------------------
+ * The attention side of a layer and what follows the LM head, for a batch of sequences
+ * that share prompts (beams, samples of one prompt, requests behind one system prompt).
+ * Lengths, page tables and parents stay on the device: no call reads them on the host, so a
+ * step of these calls can be captured in a CUDA graph and replayed as the sequences grow.
+ * The pages describe single matrices and have no counterpart.
+ *
+ * Workspaces and opts are those of the mixture-of-experts calls above.  Strides are counted
+ * in elements unless said otherwise.
+ *
+ * The paged cache: two pools, keys and values, of `pages` pages of `page` tokens; element
+ * [p][h][r][d] of a pool (page, kv head, token of the page, feature) is at
+ * p page_stride + h head_stride + r row_stride + d.  No two elements may be at the same
+ * place.  A slot names a token of the cache: page * slot's page + slot's token in it.  What
+ * the pool holds behind the last token of a sequence is never used, whatever its bits. */
+#define Q4_F16 2
+#define Q4_ROPE_HALF 0
+#define Q4_ROPE_INTERLEAVED 1
+
+typedef struct {
+    void *k, *v;               /* device, the two pools                                   */
+    int32_t dtype;             /* Q4_BF16 or Q4_F16                                       */
+    int32_t heads, D;          /* kv heads, features of a head                            */
+    int32_t page;              /* tokens of a page                                        */
+    int64_t pages;
+    int64_t page_stride, head_stride, row_stride;
+} q4_kv_cache_t;
+
+/* The new tokens' queries, keys and values (zero-initialise, then fill in). */
+typedef struct {
+    int32_t T, Hq;             /* tokens, query heads                                     */
+    int32_t dtype;             /* Q4_F32 or Q4_BF16: q, k, v                              */
+    int32_t rot;               /* features of a head that are rotated, even, <= D         */
+    int32_t layout;            /* Q4_ROPE_HALF or Q4_ROPE_INTERLEAVED                     */
+    float scale, eps;          /* factor of the cosines and sines; eps >= 0               */
+    const void *q;             /* device [T][Hq][D], token t at t * q_stride              */
+    const void *k, *v;         /* device [T][heads][D], at t * k_stride and t * v_stride;
+                                  both NULL: queries only                                 */
+    int64_t q_stride, k_stride, v_stride;
+    const float *q_gamma, *k_gamma; /* device [D] or NULL: no norm                        */
+    const int32_t *positions;  /* device [T]                                              */
+    const float *inv_freq;     /* device [rot / 2], radians per token                     */
+    const int32_t *slots;      /* device [T] or NULL: token t goes to slot t              */
+    void *q_out;               /* device [T][Hq][D], of the cache's type                  */
+    q4_kv_cache_t cache;       /* k, v: NULL where there are no keys                      */
+} q4_rope_append_t;
+
+/* Norm of each head, rotary positions, and the new tokens' keys and values into the cache:
+ *   u = x / sqrt(mean x^2 + eps) * gamma     over the D features of a head of q or k
+ *                                            (gamma NULL: x)
+ *   (u_a, u_b) -> (c u_a - s u_b, s u_a + c u_b),  c, s = scale * cos, sin of
+ *                                            positions[t] * inv_freq[i]
+ * for i < rot / 2, with (a, b) = (i, i + rot / 2) (Q4_ROPE_HALF) or (2i, 2i + 1)
+ * (Q4_ROPE_INTERLEAVED); features from rot on stay as they are.  v is copied.  All in
+ * binary32, rounded once when stored.  The angle is reduced exactly (a product of integers
+ * modulo one turn), so a far position costs no accuracy: cosines and sines are within 2^-21
+ * for any int32 position and |inv_freq| <= 16.
+ * A slot outside [0, pages * page) (-1: a padding token) is not written; of two tokens with
+ * the same slot either may stay.  inv_freq, gammas, positions and slots 4-byte aligned, q, k,
+ * v and the pools to their elements.  1 <= D <= 256 (Q4_ERR_UNSUPPORTED above).  T == 0 is
+ * an empty problem. */
+Q4_API int q4_rope_append_run(const q4_rope_append_t *args, const q4_run_options_t *opts, void *stream);
+
+/* Inverse frequencies for rot features, computed on the host in binary64 and rounded once:
+ *   f_i = base^(-2i / rot),  i < rot / 2
+ * stretched by `factor` >= 1 for contexts longer than the `trained` tokens of training:
+ *   Q4_ROPE_PLAIN   f_i
+ *   Q4_ROPE_LINEAR  f_i / factor
+ *   Q4_ROPE_BANDS   f_i where trained f_i / 2 pi, the turns within the trained context, is
+ *                   `high` or more, f_i / factor where it is `low` or less, and between
+ *                   them the mean of the two weighted linearly in the turns.
+ * inv_freq : host float [rot / 2].  low < high; low, high and trained are used by
+ * Q4_ROPE_BANDS only. */
+#define Q4_ROPE_PLAIN 0
+#define Q4_ROPE_LINEAR 1
+#define Q4_ROPE_BANDS 2
+Q4_API int q4_rope_frequencies(float *inv_freq, int32_t rot, double base, int32_t kind, double factor, double trained,
+                        double low, double high);
+
+/* Attention of S queries (zero-initialise, then fill in). */
+typedef struct {
+    int32_t S, Hq;             /* queries (one token each), query heads                   */
+    int32_t groups;            /* groups of queries; 0: no shared segments                */
+    int32_t out_dtype;         /* the cache's type, or Q4_F32                             */
+    int32_t max_shared_pages, max_own_pages; /* columns of the page tables                */
+    float scale;               /* of the products of queries and keys                     */
+    const void *q;             /* device [S][Hq][D], query s at s * q_stride              */
+    int64_t q_stride;
+    q4_kv_cache_t cache;
+    const int32_t *group_offsets; /* device [groups + 1], or NULL with one group: all     */
+    const int32_t *shared_pages;  /* device [groups][max_shared_pages]                    */
+    const int32_t *shared_lens;   /* device [groups], tokens                              */
+    const int32_t *limits;     /* device [S] or NULL                                      */
+    const int32_t *own_pages;  /* device [S][max_own_pages] or NULL: no own segments      */
+    const int32_t *own_lens;   /* device [S], tokens                                      */
+    void *out;                 /* device [S][Hq][D]                                       */
+    float *lse;                /* device [S][Hq] or NULL                                  */
+    void *workspace;
+    int64_t workspace_bytes;
+} q4_prefix_attn_t;
+
+/* Bytes of workspace q4_prefix_attn_run needs on the current device (-1 for sizes it does
+ * not serve). */
+Q4_API int64_t q4_prefix_attn_workspace(int32_t S, int32_t groups, int32_t Hq, int32_t Hkv, int32_t D);
+
+/* Attention over a segment that a group of queries shares, then each query's own segment:
+ *   o[s][h] = sum_j p_j v_j,   p = softmax(scale q[s][h] . k_j)   over the keys j of
+ *     - the first min(shared_lens[g], limits[s]) tokens named by shared_pages[g], where
+ *       group_offsets[g] <= s < group_offsets[g + 1] (limits NULL: shared_lens[g]); a query
+ *       that no group has sees no shared segment
+ *     - the first own_lens[s] tokens named by own_pages[s]
+ * of kv head h / (Hq / heads).  A query without a key gives zeros.  The shared segment is
+ * read once for all queries of a group.  With limits[s] = s + 1 and no own segments this is
+ * the causal attention of a prompt whose keys and values are in the cache.
+ * lse[s][h]: log sum_j exp(scale q . k_j), -inf without a key (natural logarithm).
+ * Lengths are clamped to [0, max pages * page], group offsets to [0, S] and to no less than
+ * the one before, and a page id outside [0, pages) reads as a page of zeros, so no content
+ * of these arrays makes the kernels leave their buffers.  Values of keys that some query of
+ * a group sees are finite; where one is not, the queries of the group that do not see it may
+ * become NaN too.
+ * Accuracy: products and sums in binary32; each weight p_j is rounded once to the cache's
+ * type (relative to the largest so far; in Q4_F16 a weight below 2^-14 of it to 2^-25 of
+ * it) before it multiplies v_j, and the sum that divides them is of unrounded weights.
+ * D is 64 or 128, page a power of two >= 16, Hq / heads an integer <= 128, S * Hq < 2^31,
+ * S <= 2^20, groups <= S, tables below 2^31 tokens a row (Q4_ERR_UNSUPPORTED outside).  q,
+ * out, the pools 16-byte aligned, and their strides multiples of 8 (Q4_ERR_MISALIGNED).  S == 0
+ * is an empty problem.  Q4_ERR_TIMEOUT from q4gemv_device_status if a bounded wait expired. */
+Q4_API int q4_prefix_attn_run(const q4_prefix_attn_t *args, const q4_run_options_t *opts, void *stream);
+
+/* Bytes of workspace q4_beam_step_run needs (-1 for sizes it does not serve). */
+Q4_API int64_t q4_beam_step_workspace(int32_t groups, int32_t W, int32_t K, int64_t V);
+
+/* One step of a beam search: the K best continuations of each group of W beams.
+ *   score(w, v) = scores[g][w] + l_v - log sum_v' exp(l_v'),  l = logits[g W + w]
+ * over all (w, v), in descending order, equal ones by lower w, then lower v.  A beam with
+ * finished[g][w] != 0 has one continuation, token eos at its own score.  NaN and infinite
+ * logits count as -inf and are never chosen; a beam whose score is not finite has no
+ * continuation.  Places left over hold token -1, parent -1, score -inf, finished 0.
+ * The order is that of the scores before they are rounded to binary32 (sums of exponentials
+ * in binary32, logarithms and scores in binary64).
+ *   logits : device float [groups W][V], row r at r * row_stride;  scores : device float
+ *   [groups][W];  finished_or_null : device uint8 [groups][W] (eos >= 0 then);
+ *   eos : a token, or -1
+ *   tokens, parents : device int32 [groups][K], parents in [0, W);  out_scores : device
+ *   float [groups][K];  out_finished_or_null : device uint8 [groups][K], 1 where the token
+ *   is eos
+ * 1 <= W <= 32, 1 <= K <= 32, V < 2^31 - 1, groups W < 2^31 (Q4_ERR_UNSUPPORTED above).
+ * groups == 0 is an empty problem. */
+Q4_API int q4_beam_step_run(const float *logits, int64_t row_stride, const float *scores, const uint8_t *finished_or_null,
+                     int32_t groups, int32_t W, int32_t K, int64_t V, int32_t eos, int32_t *tokens, int32_t *parents,
+                     float *out_scores, uint8_t *out_finished_or_null, void *workspace, int64_t workspace_bytes,
+                     const q4_run_options_t *opts, void *stream);
+
+/* Beams take over their parents' caches (zero-initialise, then fill in). */
+typedef struct {
+    int32_t groups, W;         /* sequence i = g W + w                                    */
+    int32_t max_pages;         /* columns of the page tables                              */
+    int32_t planes;            /* pools that share the tables (keys and values of layers) */
+    int32_t heads, page;       /* of a page: heads, tokens                                */
+    int64_t pages;
+    int64_t row_bytes;         /* bytes of a token of one head                            */
+    int64_t plane_stride, page_stride, head_stride, row_stride; /* bytes                  */
+    void *pool;                /* device                                                  */
+    const int32_t *tables;     /* device [groups W][max_pages]                            */
+    const int32_t *lens;       /* device [groups], tokens of each sequence of the group   */
+    const int32_t *parents;    /* device [groups][W], in [0, W)                           */
+    const int32_t *spare;      /* device [groups W], a page of its own for each sequence  */
+    int32_t *out_tables;       /* device [groups W][max_pages]                            */
+    int32_t *out_spare;        /* device [groups W]                                       */
+} q4_beam_reorder_t;
+
+/* After a beam step: sequence i continues what parent p = parents[g][w] holds.  With
+ * n = lens[g], f = n / page full pages and r = n % page tokens in the page being written:
+ *   out_tables[i][j] = tables[p][j]   for j < f: full pages are shared, not copied
+ *   out_tables[i][f] = spare[i] where r > 0 and p != i, tables[i][f] otherwise; in the first
+ *     case rows [0, r) of page tables[p][f] are copied into page spare[i] in every plane
+ *     (the other rows stay as they are) and out_spare[i] = tables[i][f], the page that no
+ *     table names any more; otherwise out_spare[i] = spare[i]
+ *   out_tables[i][j] = tables[i][j]   for j > f
+ * The caller keeps, for each sequence, the page at tables[i][f] its own: no other table
+ * names it, and no two sequences have the same spare page.  A table column written ahead of
+ * time (page j of sequence i for all j to come) needs no host work between steps.
+ * A parent outside [0, W) counts as the sequence itself; pages outside [0, pages) are neither
+ * read nor written; lens are clamped to [0, max_pages * page] (at max_pages * page there is no
+ * page being written).  out_tables and out_spare may not overlap tables and spare.
+ * pool and strides 2-byte aligned, row_bytes even.  groups W < 2^31 (Q4_ERR_UNSUPPORTED above),
+ * 1 <= W <= 1024.  groups == 0 is an empty problem. */
+Q4_API int q4_beam_reorder_run(const q4_beam_reorder_t *args, const q4_run_options_t *opts, void *stream);
+
 /* ---- test and measurement exports (not part of the GEMV API proper) ---------------- */
 
 /* Write the dequantised matrix w[N][K] = (q - z) * s as float, with the same in-register
