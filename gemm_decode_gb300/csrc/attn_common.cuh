@@ -1,0 +1,194 @@
+// attn_common.cuh -- what the kernels of the attention over a shared and an own segment have
+// in common: how the work is divided, and where the parts of a result wait to be joined.
+//
+// Segments.  An entry is a run of queries and the keys they see: queries of a group with the
+// group's shared segment, or one query with its own.  With each kv head (and each tile of 16
+// rows in the kernel for few rows) it makes a segment: rows (query, query head of that kv
+// head) by keys.  Entries whose rows fill a tensor-core tile go to the kernel for many rows,
+// the others to the one for few; the planning kernel lists both kinds with their keys, in
+// units (tiles of keys), numbered through: entry by entry, within it segment by segment.
+//
+// Each kernel's CTAs share its units evenly, CTA c takes [c U / C, (c + 1) U / C), whatever the
+// lengths are.  A segment that falls to several CTAs leaves a part with each of them, in one
+// of two slots that a CTA has (only its first and its last segment can be shared); one that a
+// CTA holds whole goes straight to the output where nothing else can add to it, else to a
+// place by query and head.  A part is the row's sum of weighted values, relative to the
+// part's own maximum, with that maximum (in powers of two) and the sum of weights; the joining
+// kernel adds the parts of a row in the order of the keys, so results do not depend on timing.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "q4_decode.cuh"
+#include "q4_tc.cuh"
+
+namespace q4 {
+
+using namespace tc;
+
+constexpr int kManyKeys = 128, kFewKeys = 64;   // keys of a unit
+constexpr int kFewRows = 16;                    // rows of a segment of the kernel for few rows
+constexpr int kManyTiles = 2;                   // tiles of 128 rows of one segment of the kernel for many
+
+struct AttnEntry {
+    int first, queries;   // queries [first, first + queries)
+    int group;            // whose shared segment, or -1: the query's own
+    int keys;             // the most that one of the queries sees
+};
+
+struct AttnCounts {
+    int64_t units;
+    int entries;
+    int pad;
+};
+
+struct AttnArgs {
+    int S, Hq, Hkv, G, groups;   // G: query heads of a kv head
+    int D;
+    int page, page_shift, pages;
+    int box, box_shift;          // rows of a page that one copy brings
+    int max_shared, max_own;
+    int tile_queries;            // of a tile of 128 rows
+    int out_f32, alone;          // alone: a call with one kind of segment, so whole ones are final
+    float scale2;                // scale * log2(e)
+    const void *q;
+    int64_t q_stride;
+    const int *group_offsets, *shared_pages, *shared_lens, *limits, *own_pages, *own_lens;
+    void *out;
+    float *lse;
+    // workspace
+    AttnCounts *many, *few;
+    AttnEntry *many_entries, *few_entries;
+    int64_t *many_start, *few_start;   // first unit of each entry
+    int *shared_of;   // [S] entry of a query's shared segment: -1 none, >= 0 of many, -2 - e of few
+    int *own_of;      // [S] entry of few, or -1
+    int *first_of;    // [groups + 1] clamped offsets
+    int *tile_of;     // [groups + 1] first run of each group's queries
+    int *run_keys, *run_entry;   // [runs]
+    int many_ctas, few_ctas;
+    float *many_part, *few_part;     // [2 CTAs][rows][D]
+    float2 *many_stats, *few_stats;  // [2 CTAs][rows]: maximum, sum of weights
+    float *whole[2];                 // [S][Hq][D]: shared, own
+    float2 *whole_stats[2];
+    unsigned long long timeout_ns;
+    unsigned int *status;
+    unsigned int *bounds;
+};
+
+__device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ int clamp_len(int n, int most_pages, int page) {
+    const int64_t most = static_cast<int64_t>(most_pages) * page;   // below 2^31: checked by the call
+    return n < 0 ? 0 : n > most ? static_cast<int>(most) : n;
+}
+
+// CTAs that take part (each has a unit), the units that CTA c of them takes, and the CTA that
+// takes unit u.
+__device__ __forceinline__ int ctas_of(int64_t units, int most) {
+    return units < most ? static_cast<int>(units) : most;
+}
+__device__ __forceinline__ int64_t units_before(int64_t units, int ctas, int c) { return units * c / ctas; }
+__device__ __forceinline__ int owner_of(int64_t units, int ctas, int64_t u) {
+    return static_cast<int>(((u + 1) * ctas - 1) / units);
+}
+
+// Walks the segments of a CTA's share; every role of a CTA has one of its own.
+struct AttnSegment {
+    AttnEntry e;
+    int head, tile;       // kv head, tile of rows (few rows)
+    int u0, u1;           // units of the segment, [0, units) when whole
+    int units;
+    bool whole;
+    int slot;             // where a part goes: 2 * CTA + (the segment's first CTA: 1)
+};
+struct AttnWalk {
+    int64_t at, end, units;
+    int entry, ctas;
+
+    // Entry of unit `at`: the last with start <= at, by a warp (32 places a round).
+    __device__ __forceinline__ void begin(const AttnCounts *n, const int64_t *start, int count_ctas, int lane) {
+        units = __ldcg(&n->units);
+        ctas = ctas_of(units, count_ctas);
+        const bool takes_part = static_cast<int>(blockIdx.x) < ctas;
+        at = takes_part ? units_before(units, ctas, blockIdx.x) : 0;
+        end = takes_part ? units_before(units, ctas, blockIdx.x + 1) : 0;
+        int lo = 0, hi = __ldcg(&n->entries);   // start[lo] <= at < start[hi]
+        if (at >= end) return;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, p = lo + lane * step;
+            const unsigned below = __ballot_sync(~0u, p < hi && __ldcg(start + p) <= at);
+            const int k = 31 - __clz(below);   // (lane 0 always)
+            const int nlo = lo + k * step;
+            hi = min(hi, nlo + step);
+            lo = nlo;
+        }
+        entry = lo;
+    }
+    // The next segment, or false.  tiles: of 16 rows per kv head (1 in the kernel for many).
+    template <int KEYS>
+    __device__ __forceinline__ bool next(AttnSegment &s, const AttnEntry *entries, const int64_t *start, int heads,
+                                         int G, bool few) {
+        if (at >= end) return false;
+        const int4 raw = __ldcg(reinterpret_cast<const int4 *>(entries + entry));
+        s.e = AttnEntry{raw.x, raw.y, raw.z, raw.w};
+        s.units = (s.e.keys + KEYS - 1) / KEYS;
+        const int tiles = few ? (s.e.queries * G + kFewRows - 1) / kFewRows : 1;
+        const int64_t from = at - __ldcg(start + entry);
+        const int seg = static_cast<int>(from / s.units);
+        s.head = seg / tiles;
+        s.tile = seg - s.head * tiles;
+        s.u0 = static_cast<int>(from - static_cast<int64_t>(seg) * s.units);
+        s.u1 = static_cast<int>(min(static_cast<int64_t>(s.units), s.u0 + (end - at)));
+        s.whole = s.u0 == 0 && s.u1 == s.units;
+        s.slot = 2 * blockIdx.x + (s.u0 == 0 ? 1 : 0);
+        at += s.u1 - s.u0;
+        if (s.u1 == s.units && seg + 1 == heads * tiles) ++entry;
+        return true;
+    }
+};
+
+// Row `row` of a segment's rows: query and query head.
+__device__ __forceinline__ void row_of(const AttnArgs &g, const AttnSegment &s, int row, int &query, int &head) {
+    const int i = row / g.G;
+    query = s.e.first + i;
+    head = s.head * g.G + (row - i * g.G);
+}
+// Keys of the segment that a query sees.
+__device__ __forceinline__ int limit_of(const AttnArgs &g, const AttnSegment &s, int query) {
+    if (s.e.group < 0 || g.limits == nullptr) return s.e.keys;
+    return max(0, min(s.e.keys, g.limits[query]));
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z,
+                                            int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+template <typename C>
+__device__ __forceinline__ C from_f32(float v) {
+    if constexpr (std::is_same<C, __half>::value) return __float2half_rn(v);
+    else if constexpr (std::is_same<C, __nv_bfloat16>::value) return __float2bfloat16_rn(v);
+    else return v;
+}
+template <typename C>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {   // a in the lower half
+    uint32_t r;
+    if constexpr (std::is_same<C, __half>::value) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+// log sum exp, natural, from a maximum in powers of two and the sum relative to it
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l != 0.0f ? (m + log2f(l)) * 0.693147180559945f : neg_inf();
+}
+
+}  // namespace q4

@@ -67,40 +67,12 @@ struct MoeKernelArgs {
     unsigned int *bounds;
 };
 
-// Whether the phase of the given parity is complete, without suspending.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
-}
 // 16 bytes to shared memory, zeros where there is nothing to read.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool have) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(have ? 8 : 0) : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, float *f) {
     uint32_t v[16];
@@ -157,12 +129,6 @@ __device__ __forceinline__ void tmem_ld8x4(uint32_t a0, uint32_t a1, uint32_t a2
         f2[i] = __uint_as_float(v[16 + i]);
         f3[i] = __uint_as_float(v[24 + i]);
     }
-}
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
 }
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
 __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
@@ -225,26 +191,6 @@ __device__ __forceinline__ bool next_segment(MoePlan &p, MoeSegment &s) {
     s.rows = min(p.first_row[lo + 1] - s.row0, NT);
     return true;
 }
-
-// One lane of running ring position: stage and the parity its barrier is waited for with.
-template <int STAGES>
-struct Ring {
-    int s = 0;
-    uint32_t ph = 0;
-    __device__ __forceinline__ void step() {
-        if (++s == STAGES) {
-            s = 0;
-            ph ^= 1u;
-        }
-    }
-    __device__ __forceinline__ void step(int n) {   // n <= STAGES
-        s += n;
-        if (s >= STAGES) {
-            s -= STAGES;
-            ph ^= 1u;
-        }
-    }
-};
 
 // First row and first tile (of NT rows) of each expert, by one warp: offsets clamped to
 // [0, R] and to no less than the one before.
