@@ -9,7 +9,8 @@
 // units (tiles of keys), numbered through: entry by entry, within it segment by segment.
 //
 // Each kernel's CTAs share its units evenly, CTA c takes [c U / C, (c + 1) U / C), whatever the
-// lengths are.  A segment that falls to several CTAs leaves a part with each of them, in one
+// lengths are; a segment counts for some units more than it has, for what its beginning and
+// its end cost.  A segment that falls to several CTAs leaves a part with each of them, in one
 // of two slots that a CTA has (only its first and its last segment can be shared); one that a
 // CTA holds whole goes straight to the output where nothing else can add to it, else to a
 // place by query and head.  A part is the row's sum of weighted values, relative to the
@@ -29,6 +30,7 @@ namespace q4 {
 using namespace tc;
 
 constexpr int kManyKeys = 128, kFewKeys = 64;   // keys of a unit
+constexpr int kManyCost = 1, kFewCost = 1;      // units that a segment's beginning and end count for
 constexpr int kFewRows = 16;                    // rows of a segment of the kernel for few rows
 constexpr int kManyTiles = 2;                   // tiles of 128 rows of one segment of the kernel for many
 
@@ -38,8 +40,17 @@ struct AttnEntry {
     int keys;             // the most that one of the queries sees
 };
 
+// Where the joining kernel finds the parts of a query's rows of one entry.
+struct alignas(16) AttnPlace {
+    int64_t start;        // the entry's first unit
+    int units;            // of a segment; 0: the query sees no key of this kind
+    int many;             // kernel: many rows (1) or few
+    int place, tiles;     // the query's place in its entry; tiles of 16 rows per kv head (few rows)
+    int pad[2];
+};
+
 struct AttnCounts {
-    int64_t units;
+    int64_t units;   // with the cost of each segment
     int entries;
     int pad;
 };
@@ -62,11 +73,11 @@ struct AttnArgs {
     AttnCounts *many, *few;
     AttnEntry *many_entries, *few_entries;
     int64_t *many_start, *few_start;   // first unit of each entry
-    int *shared_of;   // [S] entry of a query's shared segment: -1 none, >= 0 of many, -2 - e of few
-    int *own_of;      // [S] entry of few, or -1
-    int *first_of;    // [groups + 1] clamped offsets
-    int *tile_of;     // [groups + 1] first run of each group's queries
-    int *run_keys, *run_entry;   // [runs]
+    AttnPlace *places;   // [2][S]: shared, own
+    int *first_of;       // [groups + 1] clamped offsets
+    int *run_of;         // [groups + 1] first run of each group's queries
+    int *run_keys;       // [runs] the most keys that a query of the run sees
+    int64_t *run_start;  // [runs] first unit of the run
     int many_ctas, few_ctas;
     float *many_part, *few_part;     // [2 CTAs][rows][D]
     float2 *many_stats, *few_stats;  // [2 CTAs][rows]: maximum, sum of weights
@@ -107,50 +118,78 @@ struct AttnSegment {
     bool whole;
     int slot;             // where a part goes: 2 * CTA + (the segment's first CTA: 1)
 };
+// The first entries of a CTA's share, in shared memory.
+struct AttnHeld {
+    static constexpr int kMost = 32;
+    int4 entry[kMost];
+    int64_t start[kMost];
+};
+template <int KEYS, int COST, bool FEW>
 struct AttnWalk {
-    int64_t at, end, units;
-    int entry, ctas;
+    int64_t at, end;
+    int entry, first;
+    const AttnHeld *held;
+    const AttnEntry *entries;
+    const int64_t *start;
 
-    // Entry of unit `at`: the last with start <= at, by a warp (32 places a round).
-    __device__ __forceinline__ void begin(const AttnCounts *n, const int64_t *start, int count_ctas, int lane) {
-        units = __ldcg(&n->units);
-        ctas = ctas_of(units, count_ctas);
+    // To the entry of unit `at`, the last with start <= at: by a warp, 32 places a round.
+    __device__ __forceinline__ void begin(const AttnCounts *n, const AttnEntry *all, const int64_t *starts, int most,
+                                          int lane) {
+        const int4 raw = __ldcg(reinterpret_cast<const int4 *>(n));
+        const int64_t units = static_cast<int64_t>(static_cast<uint32_t>(raw.x)) | static_cast<int64_t>(raw.y) << 32;
+        const int ctas = ctas_of(units, most);
         const bool takes_part = static_cast<int>(blockIdx.x) < ctas;
+        entries = all;
+        start = starts;
         at = takes_part ? units_before(units, ctas, blockIdx.x) : 0;
         end = takes_part ? units_before(units, ctas, blockIdx.x + 1) : 0;
-        int lo = 0, hi = __ldcg(&n->entries);   // start[lo] <= at < start[hi]
-        if (at >= end) return;
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 31) / 32, p = lo + lane * step;
-            const unsigned below = __ballot_sync(~0u, p < hi && __ldcg(start + p) <= at);
-            const int k = 31 - __clz(below);   // (lane 0 always)
-            const int nlo = lo + k * step;
-            hi = min(hi, nlo + step);
-            lo = nlo;
+        int lo = 0, hi = raw.z;   // start[lo] <= at < start[hi]
+        if (at < end)
+            while (hi - lo > 1) {
+                const int step = (hi - lo + 31) / 32, p = lo + lane * step;
+                const unsigned below = __ballot_sync(~0u, p < hi && __ldcg(start + p) <= at);
+                const int k = 31 - __clz(below);   // (lane 0 always)
+                lo += k * step;
+                hi = min(hi, lo + step);
+            }
+        entry = first = lo;
+        left_ = raw.z - lo;
+    }
+    // The entries from the first on into shared memory, by all threads (a barrier is to follow).
+    __device__ __forceinline__ void hold(AttnHeld *to) {
+        held = to;
+        const int i = threadIdx.x;
+        if (i < AttnHeld::kMost && i < left_ && at < end) {
+            to->entry[i] = __ldcg(reinterpret_cast<const int4 *>(entries + first + i));
+            to->start[i] = __ldcg(start + first + i);
         }
-        entry = lo;
     }
-    // The next segment, or false.  tiles: of 16 rows per kv head (1 in the kernel for many).
-    template <int KEYS>
-    __device__ __forceinline__ bool next(AttnSegment &s, const AttnEntry *entries, const int64_t *start, int heads,
-                                         int G, bool few) {
-        if (at >= end) return false;
-        const int4 raw = __ldcg(reinterpret_cast<const int4 *>(entries + entry));
-        s.e = AttnEntry{raw.x, raw.y, raw.z, raw.w};
-        s.units = (s.e.keys + KEYS - 1) / KEYS;
-        const int tiles = few ? (s.e.queries * G + kFewRows - 1) / kFewRows : 1;
-        const int64_t from = at - __ldcg(start + entry);
-        const int seg = static_cast<int>(from / s.units);
-        s.head = seg / tiles;
-        s.tile = seg - s.head * tiles;
-        s.u0 = static_cast<int>(from - static_cast<int64_t>(seg) * s.units);
-        s.u1 = static_cast<int>(min(static_cast<int64_t>(s.units), s.u0 + (end - at)));
-        s.whole = s.u0 == 0 && s.u1 == s.units;
-        s.slot = 2 * blockIdx.x + (s.u0 == 0 ? 1 : 0);
-        at += s.u1 - s.u0;
-        if (s.u1 == s.units && seg + 1 == heads * tiles) ++entry;
-        return true;
+    // The next segment, or false.
+    __device__ __forceinline__ bool next(AttnSegment &s, int heads, int G) {
+        while (at < end) {
+            const int i = entry - first;
+            const int4 raw = i < AttnHeld::kMost ? held->entry[i] : __ldcg(reinterpret_cast<const int4 *>(entries + entry));
+            const int64_t from = at - (i < AttnHeld::kMost ? held->start[i] : __ldcg(start + entry));
+            s.e = AttnEntry{raw.x, raw.y, raw.z, raw.w};
+            s.units = (s.e.keys + KEYS - 1) / KEYS;
+            const int each = s.units + COST, tiles = FEW ? (s.e.queries * G + kFewRows - 1) / kFewRows : 1;
+            const int seg = static_cast<int>(from / each), off = static_cast<int>(from - static_cast<int64_t>(seg) * each);
+            const int take = static_cast<int>(min(static_cast<int64_t>(each - off), end - at));
+            at += take;
+            if (off + take == each && seg + 1 == heads * tiles) ++entry;
+            s.head = seg / tiles;
+            s.tile = seg - s.head * tiles;
+            s.u0 = max(off - COST, 0);
+            s.u1 = off + take - COST;
+            s.whole = s.u0 == 0 && s.u1 == s.units;
+            s.slot = 2 * blockIdx.x + (s.u0 == 0 ? 1 : 0);
+            if (s.u1 > s.u0) return true;
+        }
+        return false;
     }
+
+private:
+    int left_;
 };
 
 // Row `row` of a segment's rows: query and query head.

@@ -26,10 +26,10 @@ struct FewAttn {
     static constexpr int kTileBytes = kFewKeys * D * 2;            // keys or values of a unit
     static constexpr int kStageBytes = 2 * kTileBytes;
     static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kBars = 2 * kStages;
+    static constexpr int kBars = 2 * kStages;   // (an even number: what follows is aligned to 16 bytes)
     static constexpr int kJoinBytes = kFewRows * D * 4;            // one warp's accumulators
     static constexpr size_t smem() {
-        return 1024 + static_cast<size_t>(kStages) * kStageBytes + kJoinBytes + 8 * kBars + kWarps * kFewRows * 8 + 16;
+        return 1024 + static_cast<size_t>(kStages) * kStageBytes + kJoinBytes + 8 * kBars + kWarps * kFewRows * 8 + sizeof(AttnHeld) + 16;
     }
 };
 
@@ -71,7 +71,8 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     float *join = reinterpret_cast<float *>(ring + F::kStages * F::kStageBytes);
     uint64_t *bars = reinterpret_cast<uint64_t *>(join + kFewRows * D);
     float2 *stats = reinterpret_cast<float2 *>(bars + F::kBars);   // [warps][16 rows]
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(stats + F::kWarps * kFewRows);
+    AttnHeld *held = reinterpret_cast<AttnHeld *>(stats + F::kWarps * kFewRows);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(held + 1);
     const int warp = __shfl_sync(~0u, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const unsigned long long limit_ns = g.timeout_ns;
     auto ib = [&](bool ok) { return q4_in_bounds(ok, g.bounds); };
@@ -104,8 +105,10 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         return false;
     };
 
-    AttnWalk walk;
-    walk.begin(g.few, g.few_start, g.few_ctas, lane);
+    AttnWalk<kFewKeys, kFewCost, true> walk;
+    walk.begin(g.few, g.few_entries, g.few_start, g.few_ctas, lane);
+    walk.hold(held);
+    __syncthreads();
     AttnSegment s;
 
     if (warp == F::kWarps) {
@@ -118,7 +121,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         const int box = lane % boxes, half = lane / boxes % F::kHalves, kv = lane / (boxes * F::kHalves);
         const uint32_t to = smem_addr(ring) + kv * F::kTileBytes + half * (kFewKeys * 128) + (box << g.box_shift) * 128;
         const CUtensorMap *map = kv == 0 ? &map_k : &map_v;
-        while (ok && walk.next<kFewKeys>(s, g.few_entries, g.few_start, g.Hkv, g.G, true)) {
+        while (ok && walk.next(s, g.Hkv, g.G)) {
             const int *table = s.e.group < 0 ? g.own_pages + static_cast<int64_t>(s.e.first) * g.max_own
                                              : g.shared_pages + static_cast<int64_t>(s.e.group) * g.max_shared;
             auto page_of = [&](int u) {   // the lane's page of unit u; one outside the pool reads as zeros
@@ -171,7 +174,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
             : "memory");
         return a != 0;
     };
-    while (ok && walk.next<kFewKeys>(s, g.few_entries, g.few_start, g.Hkv, g.G, true)) {
+    while (ok && walk.next(s, g.Hkv, g.G)) {
         const int rows = min(kFewRows, s.e.queries * g.G - s.tile * kFewRows);
         // operand A: the rows' queries
         uint32_t q[kK][4];

@@ -11,12 +11,12 @@
 // than a factor of 2^8: weights up to 2^8 round as well as ones below 1, sums are binary32, and
 // the sums in tensor memory hardly ever have to be scaled.
 //
-// One CTA per SM, ten warps:
+// One CTA per SM, twelve warps:
 //   warp 0      bulk tensor copies: queries of a segment, tiles of keys and values in turn into
 //               one ring of stages (a box per page, or 64 rows of one; a lane each)
 //   warp 1      the MMAs: the warp walks the loop, one elected lane issues.  The scores of one
 //               tile of rows are formed while the weights of the other are computed.
-//   warps 2-5, 6-9   weights of the first and second tile of rows, and the results
+//   warps 4-7, 8-11  weights of the first and second tile of rows, and the results
 #pragma once
 
 #include "attn_common.cuh"
@@ -25,15 +25,15 @@ namespace q4 {
 
 template <int D>
 struct ManyAttn {
-    static constexpr int kThreads = 320;
+    static constexpr int kThreads = 384;
     static constexpr int kHalves = D / 64;
     static constexpr int kHalfBytes = kManyKeys * 128;            // 128 rows of 64 features
     static constexpr int kTileBytes = kHalves * kHalfBytes;       // queries of a tile, keys or values of one
     static constexpr int kStages = D == 128 ? 5 : 8;
-    static constexpr int kBars = 2 * kStages + 12;
+    static constexpr int kBars = 2 * kStages + 14;   // (an even number: what follows is aligned to 16 bytes)
     static constexpr int kTmemCols = 512;
     static constexpr size_t smem() {
-        return 1024 + static_cast<size_t>(kManyTiles + kStages) * kTileBytes + 8 * kBars + 16;
+        return 1024 + static_cast<size_t>(kManyTiles + kStages) * kTileBytes + 8 * kBars + sizeof(AttnHeld) + 16;
     }
 };
 
@@ -79,6 +79,16 @@ __device__ __forceinline__ void pin32(float *f) {
                      : "+f"(f[i]), "+f"(f[i + 1]), "+f"(f[i + 2]), "+f"(f[i + 3]), "+f"(f[i + 4]), "+f"(f[i + 5]),
                        "+f"(f[i + 6]), "+f"(f[i + 7]));
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const float *f) {
     tmem_st16(addr, reinterpret_cast<const uint32_t *>(f));
@@ -95,7 +105,8 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *q_tiles = smem, *ring = smem + kManyTiles * M::kTileBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + M::kStages * M::kTileBytes);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + M::kBars);
+    AttnHeld *held = reinterpret_cast<AttnHeld *>(bars + M::kBars);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(held + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = __shfl_sync(~0u, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const unsigned long long limit_ns = g.timeout_ns;
@@ -106,9 +117,9 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     auto other = [&](int i) { return bar0 + 8u * (2 * M::kStages + i); };
     const uint32_t q_full = other(0), q_empty = other(1), done = other(2);
     auto s_full = [&](int t) { return other(3 + t); };    // scores of a tile of rows are there
-    auto p_full = [&](int t) { return other(5 + t); };    // its weights are
-    auto o_full = [&](int t) { return other(7 + t); };    // its results are
-    auto o_empty = [&](int t) { return other(9 + t); };   // its results have been read
+    auto p_full = [&](int t, int half) { return other(5 + 2 * t + half); };   // the weights of half its keys are
+    auto o_full = [&](int t) { return other(9 + t); };    // its results are
+    auto o_empty = [&](int t) { return other(11 + t); };  // its results have been read
     if (threadIdx.x == 0) {
         for (int s = 0; s < M::kStages; ++s) {
             mbar_init(full(s), 1);
@@ -119,7 +130,8 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(done, 1);
         for (int t = 0; t < kManyTiles; ++t) {
             mbar_init(s_full(t), 1);
-            mbar_init(p_full(t), 4);
+            mbar_init(p_full(t, 0), 4);
+            mbar_init(p_full(t, 1), 4);
             mbar_init(o_full(t), 1);
             mbar_init(o_empty(t), 4);
         }
@@ -151,14 +163,18 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         atomicOr(g.status, 1u);
         return false;
     };
-    auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(~0u, wait(bar, parity)); };
-
-    AttnWalk walk;
-    walk.begin(g.many, g.many_start, g.many_ctas, lane);
+    auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(~0u, wait(bar, parity)) != 0; };
+    AttnWalk<kManyKeys, kManyCost, false> walk;
+    walk.begin(g.many, g.many_entries, g.many_start, g.many_ctas, lane);
+    walk.hold(held);
+    __syncthreads();
     AttnSegment s;
-    auto next = [&]() { return walk.next<kManyKeys>(s, g.many_entries, g.many_start, g.Hkv, g.G, false); };
+    auto next = [&]() { return walk.next(s, g.Hkv, g.G); };
     const uint32_t s_cols = 0, o_cols = kManyTiles * kManyKeys;   // tensor memory: scores, results
 
+    // registers: 384 x 168 at the launch, 128 x 88 + 256 x 208 from here on
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
         // ------------------------------------------------------------ copies
         Ring<M::kStages> r;
@@ -179,17 +195,6 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 return id < 0 || id > g.pages ? g.pages : id;
             };
             int page = page_of(s.u0);
-            if (!wait_all(q_empty, q_ph ^ 1u)) break;
-            q_ph ^= 1u;
-            if (lane == 0)
-                mbar_expect_tx(q_full, static_cast<uint32_t>(tiles * M::kHalves * g.tile_queries * g.G * 128));
-            __syncwarp();
-            if (lane < tiles * M::kHalves) {
-                const int t = lane / M::kHalves, h = lane - t * M::kHalves;
-                tma_load_3d(smem_addr(q_tiles) + t * M::kTileBytes + h * M::kHalfBytes, &map_q, q_full, h * 64,
-                            s.head * g.G, s.e.first + t * g.tile_queries);
-            }
-            ++queries;
             for (int u = s.u0; ok && u < s.u1; ++u) {
                 const int after = u + 1 < s.u1 ? page_of(u + 1) : 0;
 #pragma unroll
@@ -205,6 +210,22 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                     (u * kManyKeys + (box << g.box_shift)) & (g.page - 1), s.head, page);
                     r.step();
                     ++issued;
+                    if (u == s.u0 && kv == 0) {   // the queries, as soon as the segment before needs its own no more
+                        if (!wait_all(q_empty, q_ph ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        q_ph ^= 1u;
+                        if (lane == 0)
+                            mbar_expect_tx(q_full, static_cast<uint32_t>(tiles * M::kHalves * g.tile_queries * g.G * 128));
+                        __syncwarp();
+                        if (lane < tiles * M::kHalves) {
+                            const int t = lane / M::kHalves, h = lane - t * M::kHalves;
+                            tma_load_3d(smem_addr(q_tiles) + t * M::kTileBytes + h * M::kHalfBytes, &map_q, q_full,
+                                        h * 64, s.head * g.G, s.e.first + t * g.tile_queries);
+                        }
+                        ++queries;
+                    }
                 }
                 page = after;
             }
@@ -278,8 +299,20 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             __syncwarp();
                         }
                     }
-                    if (!wait_all(p_full(t), p_ph[t]) || (u == s.u0 && !wait_all(o_empty(t), oe_ph[t] ^ 1u)) ||
-                        (more && t == 0 && !wait_all(full(ks), k_ph))) {
+                    if (!wait_all(p_full(t, 0), p_ph[t]) || (u == s.u0 && !wait_all(o_empty(t), oe_ph[t] ^ 1u))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t b = v_desc + static_cast<uint32_t>(vs) * (M::kTileBytes / 16);
+                    const uint32_t a = tmem + s_cols + t * kManyKeys, d = tmem + o_cols + t * D;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kManyKeys / 32; ++k)
+                            umma_f16_ts(d, a + k * 8, b + k * (2048 / 16), idesc_o, k > 0 || u > s.u0 ? 1u : 0u);
+                    }
+                    __syncwarp();
+                    if (!wait_all(p_full(t, 1), p_ph[t]) || (more && t == 0 && !wait_all(full(ks), k_ph))) {
                         ok = false;
                         break;
                     }
@@ -287,11 +320,9 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     if (u == s.u0) oe_ph[t] ^= 1u;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint64_t b = v_desc + static_cast<uint32_t>(vs) * (M::kTileBytes / 16);
-                        const uint32_t a = tmem + s_cols + t * kManyKeys, d = tmem + o_cols + t * D;
 #pragma unroll
-                        for (int k = 0; k < kManyKeys / 16; ++k)
-                            umma_f16_ts(d, a + k * 8, b + k * (2048 / 16), idesc_o, k > 0 || u > s.u0 ? 1u : 0u);
+                        for (int k = kManyKeys / 32; k < kManyKeys / 16; ++k)
+                            umma_f16_ts(d, a + k * 8, b + k * (2048 / 16), idesc_o, 1u);
                         if (!more) umma_commit(o_full(t));
                         else scores(t, ks);
                         if (t == tiles - 1) {
@@ -306,9 +337,11 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         }
         if (elect_one()) umma_commit(done);   // every MMA issued (waited for before tensor memory is freed)
         __syncwarp();
+    }
     } else {
         // ------------------------------------------------------------ weights and results
-        const int t = warp < 6 ? 0 : 1;                       // tile of rows
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = (warp >> 2) - 1;                        // tile of rows
         const int row = (warp & 3) * 32 + lane;               // lane of tensor memory
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + s_cols + t * kManyKeys, o_at = tmem + lanes + o_cols + t * D;
@@ -343,22 +376,41 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     for (int c = 0; c < kManyKeys; ++c)
                         if (c >= seen) x[c] = off;
                 }
-                // the largest score (the smallest, times a scale below zero)
-                float top = x[0], top1 = x[1], top2 = x[2], top3 = x[3];
+                // The weights of half the keys, relative to the maximum so far, and meanwhile the
+                // largest score (the smallest, times a scale below zero): only where that has
+                // outgrown the maximum, the weights are formed again.
+                uint32_t p[kManyKeys / 2];
+                float2 sum[2];
+                auto weigh = [&](int half) {
+                    const float b = m == neg_inf() ? 0.0f : -m;
+                    const float2 base = make_float2(b, b), scale = make_float2(g.scale2, g.scale2);
+#pragma unroll
+                    for (int i = half * 64; i < half * 64 + 64; i += 2) {
+                        const float2 y = __ffma2_rn(make_float2(x[i], x[i + 1]), scale, base);
+                        const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                        sum[(i / 2) % 2] = __fadd2_rn(sum[(i / 2) % 2], e);
+                        p[i / 2] = pack2<C>(e.x, e.y);
+                    }
+                };
+                sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+                weigh(0);
+                float top;
                 if (g.scale2 >= 0.0f) {
+                    float a = max3(x[0], x[1], x[2]), b = max3(x[3], x[4], x[5]);
 #pragma unroll
-                    for (int c = 4; c < kManyKeys; c += 4) {
-                        top = fmaxf(top, x[c]), top1 = fmaxf(top1, x[c + 1]);
-                        top2 = fmaxf(top2, x[c + 2]), top3 = fmaxf(top3, x[c + 3]);
+                    for (int c = 6; c + 3 < kManyKeys; c += 4) {
+                        a = max3(a, x[c], x[c + 1]);
+                        b = max3(b, x[c + 2], x[c + 3]);
                     }
-                    top = fmaxf(fmaxf(top, top1), fmaxf(top2, top3));
+                    top = max3(a, b, fmaxf(x[kManyKeys - 2], x[kManyKeys - 1]));
                 } else {
+                    float a = min3(x[0], x[1], x[2]), b = min3(x[3], x[4], x[5]);
 #pragma unroll
-                    for (int c = 4; c < kManyKeys; c += 4) {
-                        top = fminf(top, x[c]), top1 = fminf(top1, x[c + 1]);
-                        top2 = fminf(top2, x[c + 2]), top3 = fminf(top3, x[c + 3]);
+                    for (int c = 6; c + 3 < kManyKeys; c += 4) {
+                        a = min3(a, x[c], x[c + 1]);
+                        b = min3(b, x[c + 2], x[c + 3]);
                     }
-                    top = fminf(fminf(top, top1), fminf(top2, top3));
+                    top = min3(a, b, fminf(x[kManyKeys - 2], x[kManyKeys - 1]));
                 }
                 top *= g.scale2;
                 const bool renew = have && (top > m + 8.0f || (m == neg_inf() && top > m));
@@ -381,27 +433,21 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             tmem_st32(o_at + c, v);
                         }
                     }
+                    sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+                    weigh(0);
                 }
-                const float base = m == neg_inf() ? 0.0f : m;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int c = 0; c < kManyKeys; c += 32) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float a = exp2_fast(fmaf(x[c + i], g.scale2, -base));
-                        const float b = exp2_fast(fmaf(x[c + i + 1], g.scale2, -base));
-                        sum[i % 4] += a;
-                        sum[i % 4 + 1] += b;
-                        p[i / 2] = pack2<C>(a, b);
-                    }
-                    tmem_st16(s_at + c / 2, p);
+                for (int half = 0; half < 2; ++half) {
+                    if (half == 1) weigh(1);
+                    tmem_st16(s_at + half * 32, p + half * 32);
+                    tmem_st16(s_at + half * 32 + 16, p + half * 32 + 16);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(t, half));   // half the keys: their products may begin
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(t));
+                sum[0] = __fadd2_rn(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
             }
             if (!ok || !wait_all(o_full(t), o_ph)) break;
             o_ph ^= 1u;

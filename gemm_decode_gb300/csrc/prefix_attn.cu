@@ -26,7 +26,7 @@ constexpr int kJoinThreads = 256;
 
 // Inclusive sums of a and b over the block, in place; the totals in ta and tb.
 __device__ __forceinline__ void block_scan(int64_t &a, int &b, int64_t &ta, int &tb, int64_t *sa, int *sb) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t na = __shfl_up_sync(~0u, a, o);
@@ -36,8 +36,8 @@ __device__ __forceinline__ void block_scan(int64_t &a, int &b, int64_t &ta, int 
     __syncthreads();   // (sa and sb may still be read from the call before)
     if (lane == 31) sa[warp] = a, sb[warp] = b;
     __syncthreads();
-    int64_t wa = sa[lane];
-    int wb = sb[lane];
+    int64_t wa = lane < warps ? sa[lane] : 0;
+    int wb = lane < warps ? sb[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t na = __shfl_up_sync(~0u, wa, o);
@@ -52,118 +52,126 @@ __device__ __forceinline__ void block_scan(int64_t &a, int &b, int64_t &ta, int 
     }
 }
 
+// Inclusive running maximum over the block.
+__device__ __forceinline__ int block_max_scan(int v, int &total, int *sb) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v = max(v, n);
+    }
+    __syncthreads();
+    if (lane == 31) sb[warp] = v;
+    __syncthreads();
+    int w = lane < warps ? sb[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(~0u, w, o);
+        if (lane >= o) w = max(w, n);
+    }
+    total = __shfl_sync(~0u, w, 31);
+    const int before = __shfl_sync(~0u, w, max(warp - 1, 0));
+    return warp > 0 ? max(v, before) : v;
+}
+
+// The last i of [0, n) with at[i] <= v (at ascending, at[0] <= v).
+__device__ __forceinline__ int last_at_most(const int *at, int n, int v) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (at[mid] <= v) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
 }  // namespace
 
+// One CTA.  A run is the queries of one entry of the kernel for many rows; tables of groups and
+// runs are in shared memory where they fit.
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs g) {
-    static_assert(kPlanThreads == 1024, "block_scan: 32 warps");
+    constexpr int kHeldGroups = 1024, kHeldRuns = 1024;
     __shared__ int64_t sa[32];
     __shared__ int sb[32];
-    const int t = threadIdx.x;
+    __shared__ int s_first[kHeldGroups + 1], s_run[kHeldGroups + 1], s_len[kHeldGroups], s_keys[kHeldRuns];
+    __shared__ int64_t s_start[kHeldRuns];
+    const int t = threadIdx.x, T = blockDim.x;
+    const bool own = g.own_lens != nullptr, held = g.groups <= kHeldGroups;
+    int *first_of = held ? s_first : g.first_of, *run_of = held ? s_run : g.run_of;
     wait_prior_grid();
     allow_next_grid();
-    const int run = kManyTiles * g.tile_queries;   // queries of an entry of the kernel for many rows
+    // what the queries' own segments need is on its way meanwhile
+    int own_len = own && t < g.S ? g.own_lens[t] : 0;
+    const int run = kManyTiles * g.tile_queries;
     auto few_group = [&](int n) { return n * g.G <= kFewRows; };
-    // ---- groups: offsets in order, and the first run of each
-    int carry_off = 0, carry_runs = 0;
-    for (int g0 = 0; g0 <= g.groups; g0 += kPlanThreads) {
-        const int i = g0 + t;
-        int off = 0;
-        if (i <= g.groups) off = g.group_offsets != nullptr ? min(max(g.group_offsets[i], 0), g.S) : (i == 0 ? 0 : g.S);
-        off = max(off, carry_off);
-        // running maximum over the block
-        {
-            const int lane = t & 31, warp = t >> 5;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int n = __shfl_up_sync(~0u, off, o);
-                if (lane >= o) off = max(off, n);
-            }
-            __syncthreads();
-            if (lane == 31) sb[warp] = off;
-            __syncthreads();
-            int w = sb[lane];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int n = __shfl_up_sync(~0u, w, o);
-                if (lane >= o) w = max(w, n);
-            }
-            carry_off = __shfl_sync(~0u, w, 31);
-            const int before = __shfl_sync(~0u, w, max(warp - 1, 0));
-            if (warp > 0) off = max(off, before);
-        }
-        if (i <= g.groups) g.first_of[i] = off;
-        __syncthreads();   // the next group's offset is written
-        int runs = 0;
-        if (i > 0 && i <= g.groups) {
-            const int n = off - g.first_of[i - 1];
-            runs = few_group(n) ? 0 : (n + run - 1) / run;
-        }
-        // place i holds the runs of group i - 1, so its inclusive sum is the first run of group i
-        int64_t dummy = 0, td;
-        int tr;
-        block_scan(dummy, runs, td, tr, sa, sb);
-        if (i <= g.groups) g.tile_of[i] = carry_runs + runs;
-        carry_runs += tr;
-    }
-    const int all_runs = carry_runs;
-    __syncthreads();
-    // ---- the most keys a run of queries sees
-    for (int i = t; i < all_runs; i += kPlanThreads) g.run_keys[i] = 0;
-    __syncthreads();
-    auto group_of = [&](int s) {   // the group with first_of[g] <= s < first_of[g + 1], or -1
-        if (g.groups == 0 || s < g.first_of[0] || s >= g.first_of[g.groups]) return -1;
-        int lo = 0, hi = g.groups;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (g.first_of[mid] <= s) lo = mid;
-            else hi = mid;
-        }
-        return lo;
-    };
+    auto group_len = [&](int group) { return held ? s_len[group] : clamp_len(g.shared_lens[group], g.max_shared, g.page); };
     auto keys_seen = [&](int group, int s) {
-        const int n = clamp_len(g.shared_lens[group], g.max_shared, g.page);
+        const int n = group_len(group);
         return g.limits != nullptr ? max(0, min(n, g.limits[s])) : n;
     };
-    for (int s = t; s < g.S; s += kPlanThreads) {
-        const int group = group_of(s);
-        int of = -1;
-        if (group >= 0) {
-            const int first = g.first_of[group];
-            if (few_group(g.first_of[group + 1] - first)) {
-                of = -2 - group;   // for now: the group
-            } else {
-                const int r = g.tile_of[group] + (s - first) / run;
-                of = r;
-                if (g.limits != nullptr || (s - first) % run == 0) atomicMax(g.run_keys + r, keys_seen(group, s));
+    // ---- groups: offsets in order, and the first run of each
+    int carry_off = 0, all_runs = 0;
+    if (g.groups > 0) {
+        for (int g0 = 0; g0 <= g.groups; g0 += T) {
+            const int i = g0 + t;
+            int off = 0;
+            if (i <= g.groups)
+                off = g.group_offsets != nullptr ? min(max(g.group_offsets[i], 0), g.S) : (i == 0 ? 0 : g.S);
+            if (held && i < g.groups) s_len[i] = clamp_len(g.shared_lens[i], g.max_shared, g.page);
+            int total;
+            off = block_max_scan(max(off, carry_off), total, sb);
+            carry_off = total;
+            if (i <= g.groups) first_of[i] = off;
+            __syncthreads();
+            // place i holds the runs of group i - 1, so its inclusive sum is the first run of group i
+            int runs = 0, tr;
+            if (i > 0 && i <= g.groups) {
+                const int n = off - first_of[i - 1];
+                runs = few_group(n) ? 0 : (n + run - 1) / run;
             }
+            int64_t none = 0, tn;
+            block_scan(none, runs, tn, tr, sa, sb);
+            if (i <= g.groups) run_of[i] = all_runs + runs;
+            all_runs += tr;
         }
-        g.shared_of[s] = of;
-        g.own_of[s] = -1;
+        __syncthreads();
     }
-    __syncthreads();
+    const bool held_runs = held && all_runs <= kHeldRuns;
+    int *run_keys = held_runs ? s_keys : g.run_keys;
+    int64_t *run_start = held_runs ? s_start : g.run_start;
+    // ---- the most keys that a query of a run sees
+    if (g.limits != nullptr && all_runs > 0) {
+        for (int i = t; i < all_runs; i += T) run_keys[i] = 0;
+        __syncthreads();
+        for (int s = t; s < g.S; s += T) {
+            if (s < first_of[0] || s >= first_of[g.groups]) continue;
+            const int group = last_at_most(first_of, g.groups, s), first = first_of[group];
+            if (!few_group(first_of[group + 1] - first))
+                atomicMax(run_keys + run_of[group] + (s - first) / run, keys_seen(group, s));
+        }
+        __syncthreads();
+    }
     // ---- entries of many rows: runs with keys
     int64_t units0 = 0;
     int entries0 = 0;
-    for (int r0 = 0; r0 < all_runs; r0 += kPlanThreads) {
+    for (int r0 = 0; r0 < all_runs; r0 += T) {
         const int r = r0 + t;
-        const int keys = r < all_runs ? __ldcg(g.run_keys + r) : 0;
-        const int64_t mine = static_cast<int64_t>((keys + kManyKeys - 1) / kManyKeys) * g.Hkv;
+        int keys = 0, group = 0;
+        if (r < all_runs) {
+            group = last_at_most(run_of, g.groups, r);
+            keys = g.limits != nullptr ? run_keys[r] : group_len(group);
+        }
+        const int64_t mine = keys > 0 ? static_cast<int64_t>((keys + kManyKeys - 1) / kManyKeys + kManyCost) * g.Hkv : 0;
         int64_t u = mine, tu;
         int e = keys > 0 ? 1 : 0, te;
         block_scan(u, e, tu, te, sa, sb);
         if (r < all_runs) {
-            const int at = entries0 + e - 1;
-            g.run_entry[r] = keys > 0 ? at : -1;
+            run_start[r] = units0 + u - mine;
+            if (g.limits == nullptr) run_keys[r] = keys;
             if (keys > 0) {
-                int lo = 0, hi = g.groups;   // the group with tile_of[g] <= r < tile_of[g + 1]
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (g.tile_of[mid] <= r) lo = mid;
-                    else hi = mid;
-                }
-                const int first = g.first_of[lo] + (r - g.tile_of[lo]) * run;
-                g.many_entries[at] = AttnEntry{first, min(run, g.first_of[lo + 1] - first), lo, keys};
-                g.many_start[at] = units0 + u - mine;
+                const int first = first_of[group] + (r - run_of[group]) * run;
+                g.many_entries[entries0 + e - 1] = AttnEntry{first, min(run, first_of[group + 1] - first), group, keys};
+                g.many_start[entries0 + e - 1] = units0 + u - mine;
             }
         }
         units0 += tu;
@@ -171,52 +179,56 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
     }
     if (t == 0) *g.many = AttnCounts{units0, entries0, 0};
     // ---- entries of few rows: own segments, then small groups
-    const bool own = g.own_lens != nullptr;
     const int places = (own ? g.S : 0) + g.groups;
     int64_t units1 = 0;
     int entries1 = 0;
-    for (int p0 = 0; p0 < places; p0 += kPlanThreads) {
+    for (int p0 = 0; p0 < places; p0 += T) {
         const int p = p0 + t;
         AttnEntry a = {0, 0, -1, 0};
-        if (p < places) {
-            if (own && p < g.S) {
-                a = AttnEntry{p, 1, -1, clamp_len(g.own_lens[p], g.max_own, g.page)};
-            } else {
-                const int group = p - (own ? g.S : 0), first = g.first_of[group], n = g.first_of[group + 1] - first;
-                if (n > 0 && few_group(n)) {
-                    int keys = 0;
+        if (own && p < g.S) {
+            a = AttnEntry{p, 1, -1, clamp_len(p0 == 0 ? own_len : g.own_lens[p], g.max_own, g.page)};
+        } else if (p < places) {
+            const int group = p - (own ? g.S : 0), first = first_of[group], n = first_of[group + 1] - first;
+            if (n > 0 && few_group(n)) {
+                int keys = 0;
+                if (g.limits == nullptr) keys = group_len(group);
+                else
                     for (int s = first; s < first + n; ++s) keys = max(keys, keys_seen(group, s));
-                    a = AttnEntry{first, n, group, keys};
-                }
+                a = AttnEntry{first, n, group, keys};
             }
         }
         const int tiles = (a.queries * g.G + kFewRows - 1) / kFewRows;
-        const int64_t mine = static_cast<int64_t>((a.keys + kFewKeys - 1) / kFewKeys) * g.Hkv * tiles;
+        const int units = (a.keys + kFewKeys - 1) / kFewKeys;
+        const int64_t mine = a.keys > 0 ? static_cast<int64_t>(units + kFewCost) * g.Hkv * tiles : 0;
         int64_t u = mine, tu;
         int e = a.keys > 0 ? 1 : 0, te;
         block_scan(u, e, tu, te, sa, sb);
+        const int64_t start = units1 + u - mine;
         if (a.keys > 0) {
-            const int at = entries1 + e - 1;
-            g.few_entries[at] = a;
-            g.few_start[at] = units1 + u - mine;
-            if (a.group < 0) g.own_of[a.first] = at;
-            else g.tile_of[a.group] = at;   // (a small group has no runs: its place is free)
-        } else if (p < places && a.group >= 0) {
-            g.tile_of[a.group] = -1;
+            g.few_entries[entries1 + e - 1] = a;
+            g.few_start[entries1 + e - 1] = start;
         }
+        if (own && p < g.S) g.places[g.S + p] = AttnPlace{start, units, 0, 0, tiles, {}};
+        if (a.group >= 0)   // a small group's queries, 16 at most
+            for (int i = 0; i < a.queries; ++i) g.places[a.first + i] = AttnPlace{start, units, 0, i, tiles, {}};
         units1 += tu;
         entries1 += te;
     }
     if (t == 0) *g.few = AttnCounts{units1, entries1, 0};
-    __syncthreads();
-    // ---- each query's entries
-    if (g.groups > 0)
-        for (int s = t; s < g.S; s += kPlanThreads) {
-            int of = g.shared_of[s];
-            if (of >= 0) of = g.run_entry[of];
-            else if (of <= -2) of = g.tile_of[-2 - of] >= 0 ? -2 - g.tile_of[-2 - of] : -1;
-            g.shared_of[s] = of;
+    // ---- the other queries' places (runs: written above, by other threads)
+    if (g.groups > 0) {
+        __syncthreads();
+        for (int s = t; s < g.S; s += T) {
+            AttnPlace at = {};
+            if (s >= first_of[0] && s < first_of[g.groups]) {
+                const int group = last_at_most(first_of, g.groups, s), first = first_of[group];
+                if (few_group(first_of[group + 1] - first)) continue;
+                const int r = (s - first) / run, keys = run_keys[run_of[group] + r];
+                at = AttnPlace{run_start[run_of[group] + r], (keys + kManyKeys - 1) / kManyKeys, 1, (s - first) - r * run, 1, {}};
+            }
+            g.places[s] = at;
         }
+    }
 }
 
 // Where the parts of a row of one segment are.
@@ -224,48 +236,37 @@ struct AttnParts {
     int count;             // 0: none
     const float *at;       // the first part's row
     const float2 *stats;
-    int64_t step;          // rows from a part to the next (but from the first to the second)
-    int64_t second;        // rows from the first to the second
+    int step;              // rows from a part to the next (but from the first to the second, half of it)
     bool final;            // already in the output
 };
 
-__device__ __forceinline__ AttnParts parts_of(const AttnArgs &g, bool many, int entry, int s, int head, int kind) {
+__device__ __forceinline__ AttnParts parts_of(const AttnArgs &g, const AttnPlace &q, const AttnCounts &n, int64_t whole,
+                                              int head, int kind) {
     AttnParts p = {};
-    const AttnEntry e = many ? g.many_entries[entry] : g.few_entries[entry];
-    const AttnCounts n = many ? *g.many : *g.few;
-    const int ctas = ctas_of(n.units, many ? g.many_ctas : g.few_ctas);
-    const int keys = many ? kManyKeys : kFewKeys;
-    const int units = (e.keys + keys - 1) / keys;
-    const int kv = head / g.G, row = (s - e.first) * g.G + (head - kv * g.G);
-    int seg = kv, at_row = row, rows;
-    if (many) {
-        rows = 128 * kManyTiles;
-        const int per = g.tile_queries * g.G;
-        at_row = row / per * 128 + row % per;
-    } else {
-        rows = kFewRows;
-        const int tiles = (e.queries * g.G + kFewRows - 1) / kFewRows;
-        seg = kv * tiles + row / kFewRows;
-        at_row = row % kFewRows;
-    }
-    const int64_t u0 = (many ? g.many_start[entry] : g.few_start[entry]) + static_cast<int64_t>(seg) * units;
-    const int c0 = owner_of(n.units, ctas, u0), c1 = owner_of(n.units, ctas, u0 + units - 1);
+    if (q.units == 0) return p;
+    const bool many = q.many != 0;
+    const int ctas = ctas_of(n.units, many ? g.many_ctas : g.few_ctas), cost = many ? kManyCost : kFewCost;
+    const int kv = head / g.G, row = q.place * g.G + (head - kv * g.G);
+    const int rows = many ? 128 * kManyTiles : kFewRows;
+    const int seg = many ? kv : kv * q.tiles + row / kFewRows;
+    const int per = g.tile_queries * g.G;
+    const int at_row = many ? (row < per ? row : row - per + 128) : row % kFewRows;
+    const int64_t u0 = q.start + static_cast<int64_t>(seg) * (q.units + cost) + cost;
+    const int c0 = owner_of(n.units, ctas, u0), c1 = owner_of(n.units, ctas, u0 + q.units - 1);
     p.count = c1 - c0 + 1;
     p.final = p.count == 1 && g.alone;
-    const float *part = many ? g.many_part : g.few_part;
-    const float2 *stats = many ? g.many_stats : g.few_stats;
-    int64_t at;
+    int64_t at = whole;
     if (p.count == 1) {
-        part = g.whole[kind];
-        stats = g.whole_stats[kind];
-        at = static_cast<int64_t>(s) * g.Hq + head;
+        p.at = g.whole[kind];
+        p.stats = g.whole_stats[kind];
     } else {
         at = static_cast<int64_t>(2 * c0 + 1) * rows + at_row;   // the first CTA's second slot, then first slots
-        p.second = rows;
+        p.at = many ? g.many_part : g.few_part;
+        p.stats = many ? g.many_stats : g.few_stats;
         p.step = 2 * rows;
     }
-    p.at = part + at * g.D;
-    p.stats = stats + at;
+    p.at += at * g.D;
+    p.stats += at;
     return p;
 }
 
@@ -283,9 +284,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     bool todo = false;
     if (lane < each && first + lane < rows) {
         const int s = static_cast<int>((first + lane) / g.Hq), head = static_cast<int>((first + lane) - static_cast<int64_t>(s) * g.Hq);
-        const int of = g.groups > 0 ? g.shared_of[s] : -1, own = g.own_lens != nullptr ? g.own_of[s] : -1;
-        if (of != -1) a = parts_of(g, of >= 0, of >= 0 ? of : -2 - of, s, head, 0);
-        if (own >= 0) b = parts_of(g, false, own, s, head, 1);
+        AttnPlace qa = {}, qb = {};
+        const AttnCounts many = *g.many, few = *g.few;
+        if (g.groups > 0) qa = g.places[s];
+        if (g.own_lens != nullptr) qb = g.places[g.S + s];
+        a = parts_of(g, qa, qa.many != 0 ? many : few, first + lane, head, 0);
+        b = parts_of(g, qb, few, first + lane, head, 1);
         todo = !(a.final || b.final);
     }
     unsigned left = __ballot_sync(~0u, todo);
@@ -301,14 +305,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
             const float *at = reinterpret_cast<const float *>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine.at), from));
             const float2 *stats =
                 reinterpret_cast<const float2 *>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine.stats), from));
-            const int64_t step = __shfl_sync(~0u, mine.step, from), second = __shfl_sync(~0u, mine.second, from);
+            const int step = __shfl_sync(~0u, mine.step, from);
+            auto place = [&](int c) { return c == 0 ? 0 : static_cast<int64_t>(2 * c - 1) * (step >> 1); };
             for (int c0 = 0; c0 < count; c0 += 32) {
                 const int n = min(32, count - c0);
                 // a part a lane: its maximum and sum, then its weight among these
                 const int c = c0 + lane;
-                const int64_t place = c == 0 ? 0 : c * step - step + second;
                 float2 st = make_float2(neg_inf(), 0.0f);
-                if (lane < n) st = __ldcg(stats + place);
+                if (lane < n) st = __ldcg(stats + place(c));
                 float top = st.x;
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
@@ -322,11 +326,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
                 l = l * old + sum;
 #pragma unroll
                 for (int i = 0; i < V; ++i) o[i] *= old;
-#pragma unroll 4
+#pragma unroll 8
                 for (int j = 0; j < n; ++j) {
                     const float f = __shfl_sync(~0u, w, j);
-                    const int cj = c0 + j;
-                    const float *src = at + (cj == 0 ? 0 : cj * step - step + second) * D + lane * V;
+                    const float *src = at + place(c0 + j) * D + lane * V;
                     if constexpr (V == 4) {
                         const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
                         o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]);
@@ -365,8 +368,8 @@ bool many_possible(int64_t S, int groups, int G) { return groups > 0 && S * G > 
 
 // Places in the workspace.
 struct Layout {
-    int64_t counts, many_entries, few_entries, many_start, few_start, shared_of, own_of, first_of, tile_of, run_keys,
-        run_entry, many_part, few_part, many_stats, few_stats, whole[2], whole_stats[2], total;
+    int64_t counts, many_entries, few_entries, many_start, few_start, places, first_of, run_of, run_keys, run_start,
+        many_part, few_part, many_stats, few_stats, whole[2], whole_stats[2], total;
     int many_ctas, few_ctas;
 };
 Layout layout_of(int S, int groups, int Hq, int Hkv, int D) {
@@ -387,12 +390,11 @@ Layout layout_of(int S, int groups, int Hq, int Hkv, int D) {
     l.few_entries = take((static_cast<int64_t>(S) + groups) * sizeof(AttnEntry));
     l.many_start = take(runs * 8);
     l.few_start = take((static_cast<int64_t>(S) + groups) * 8);
-    l.shared_of = take(4ll * S);
-    l.own_of = take(4ll * S);
+    l.places = take(2ll * S * sizeof(AttnPlace));
     l.first_of = take(4ll * (groups + 1));
-    l.tile_of = take(4ll * (groups + 1));
+    l.run_of = take(4ll * (groups + 1));
     l.run_keys = take(4 * runs);
-    l.run_entry = take(4 * runs);
+    l.run_start = take(8 * runs);
     const int64_t mrows = 2ll * l.many_ctas * 128 * kManyTiles, frows = 2ll * l.few_ctas * kFewRows;
     l.many_part = take(mrows * D * 4);
     l.many_stats = take(mrows * 8);
@@ -432,7 +434,10 @@ int launch_attn(const q4_prefix_attn_t &a, const AttnArgs &g, cudaStream_t strea
     CUtensorMap map_k, map_v, map_q;
     if (!encode(&map_k, c.dtype, c.k, 4, dims, strides, box) || !encode(&map_v, c.dtype, c.v, 4, dims, strides, box))
         return Q4_ERR_UNSUPPORTED;
-    int st = launch_overlappable(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, call_options().overlap, g);
+    // no more warps than there are queries or groups: each barrier costs by the warp
+    const int places = std::max(a.S, a.groups + 1);
+    const unsigned threads = static_cast<unsigned>(std::min(kPlanThreads, (places + 31) / 32 * 32));
+    int st = launch_overlappable(attn_plan_kernel, dim3(1), dim3(threads), 0, stream, call_options().overlap, g);
     if (st != Q4_OK) return st;
     if (g.many_ctas > 0) {
         using M = ManyAttn<D>;
@@ -516,12 +521,11 @@ int launch_prefix_attn(const q4_prefix_attn_t &a, cudaStream_t stream) {
     g.few_entries = reinterpret_cast<AttnEntry *>(w + l.few_entries);
     g.many_start = reinterpret_cast<int64_t *>(w + l.many_start);
     g.few_start = reinterpret_cast<int64_t *>(w + l.few_start);
-    g.shared_of = reinterpret_cast<int *>(w + l.shared_of);
-    g.own_of = reinterpret_cast<int *>(w + l.own_of);
+    g.places = reinterpret_cast<AttnPlace *>(w + l.places);
     g.first_of = reinterpret_cast<int *>(w + l.first_of);
-    g.tile_of = reinterpret_cast<int *>(w + l.tile_of);
+    g.run_of = reinterpret_cast<int *>(w + l.run_of);
     g.run_keys = reinterpret_cast<int *>(w + l.run_keys);
-    g.run_entry = reinterpret_cast<int *>(w + l.run_entry);
+    g.run_start = reinterpret_cast<int64_t *>(w + l.run_start);
     g.many_ctas = l.many_ctas;
     g.few_ctas = l.few_ctas;
     g.many_part = reinterpret_cast<float *>(w + l.many_part);
