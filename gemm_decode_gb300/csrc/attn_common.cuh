@@ -104,9 +104,27 @@ __device__ __forceinline__ int clamp_len(int n, int most_pages, int page) {
 __device__ __forceinline__ int ctas_of(int64_t units, int most) {
     return units < most ? static_cast<int>(units) : most;
 }
-__device__ __forceinline__ int64_t units_before(int64_t units, int ctas, int c) { return units * c / ctas; }
+// (divisions in 32 bits where the numbers allow it: in 64 they take several hundred cycles)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+__device__ __forceinline__ int64_t units_before(int64_t units, int ctas, int c) { return quotient(units * c, ctas); }
 __device__ __forceinline__ int owner_of(int64_t units, int ctas, int64_t u) {
-    return static_cast<int>(((u + 1) * ctas - 1) / units);
+    return static_cast<int>(quotient((u + 1) * ctas - 1, units));
+}
+
+// The entry of unit u: the last of `n` with start <= u, by a warp, 32 places a round.
+__device__ __forceinline__ int entry_at(const int64_t *start, int n, int64_t u, int lane) {
+    int lo = 0, hi = n;   // start[lo] <= u < start[hi]
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, p = lo + lane * step;
+        const unsigned below = __ballot_sync(~0u, p < hi && __ldcg(start + p) <= u);
+        const int k = 31 - __clz(below);   // (lane 0 always)
+        lo += k * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
 }
 
 // Walks the segments of a CTA's share; every role of a CTA has one of its own.
@@ -132,7 +150,7 @@ struct AttnWalk {
     const AttnEntry *entries;
     const int64_t *start;
 
-    // To the entry of unit `at`, the last with start <= at: by a warp, 32 places a round.
+    // To the CTA's first unit, by a warp.
     __device__ __forceinline__ void begin(const AttnCounts *n, const AttnEntry *all, const int64_t *starts, int most,
                                           int lane) {
         const int4 raw = __ldcg(reinterpret_cast<const int4 *>(n));
@@ -143,15 +161,7 @@ struct AttnWalk {
         start = starts;
         at = takes_part ? units_before(units, ctas, blockIdx.x) : 0;
         end = takes_part ? units_before(units, ctas, blockIdx.x + 1) : 0;
-        int lo = 0, hi = raw.z;   // start[lo] <= at < start[hi]
-        if (at < end)
-            while (hi - lo > 1) {
-                const int step = (hi - lo + 31) / 32, p = lo + lane * step;
-                const unsigned below = __ballot_sync(~0u, p < hi && __ldcg(start + p) <= at);
-                const int k = 31 - __clz(below);   // (lane 0 always)
-                lo += k * step;
-                hi = min(hi, lo + step);
-            }
+        const int lo = at < end ? entry_at(start, raw.z, at, lane) : 0;
         entry = first = lo;
         left_ = raw.z - lo;
     }
@@ -173,7 +183,7 @@ struct AttnWalk {
             s.e = AttnEntry{raw.x, raw.y, raw.z, raw.w};
             s.units = (s.e.keys + KEYS - 1) / KEYS;
             const int each = s.units + COST, tiles = FEW ? (s.e.queries * G + kFewRows - 1) / kFewRows : 1;
-            const int seg = static_cast<int>(from / each), off = static_cast<int>(from - static_cast<int64_t>(seg) * each);
+            const int seg = static_cast<int>(quotient(from, each)), off = static_cast<int>(from - static_cast<int64_t>(seg) * each);
             const int take = static_cast<int>(min(static_cast<int64_t>(each - off), end - at));
             at += take;
             if (off + take == each && seg + 1 == heads * tiles) ++entry;

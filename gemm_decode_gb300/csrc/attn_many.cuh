@@ -23,6 +23,10 @@
 
 namespace q4 {
 
+// The weights of a tile are handed over in two parts: those of the first keys, whose products
+// take as long as the other weights do.
+constexpr int kFirstKeys = 96;
+
 template <int D>
 struct ManyAttn {
     static constexpr int kThreads = 384;
@@ -117,7 +121,7 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     auto other = [&](int i) { return bar0 + 8u * (2 * M::kStages + i); };
     const uint32_t q_full = other(0), q_empty = other(1), done = other(2);
     auto s_full = [&](int t) { return other(3 + t); };    // scores of a tile of rows are there
-    auto p_full = [&](int t, int half) { return other(5 + 2 * t + half); };   // the weights of half its keys are
+    auto p_full = [&](int t, int part) { return other(5 + 2 * t + part); };   // the weights of its first keys are, of all
     auto o_full = [&](int t) { return other(9 + t); };    // its results are
     auto o_empty = [&](int t) { return other(11 + t); };  // its results have been read
     if (threadIdx.x == 0) {
@@ -308,7 +312,7 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     const uint32_t a = tmem + s_cols + t * kManyKeys, d = tmem + o_cols + t * D;
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < kManyKeys / 32; ++k)
+                        for (int k = 0; k < kFirstKeys / 16; ++k)
                             umma_f16_ts(d, a + k * 8, b + k * (2048 / 16), idesc_o, k > 0 || u > s.u0 ? 1u : 0u);
                     }
                     __syncwarp();
@@ -321,7 +325,7 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = kManyKeys / 32; k < kManyKeys / 16; ++k)
+                        for (int k = kFirstKeys / 16; k < kManyKeys / 16; ++k)
                             umma_f16_ts(d, a + k * 8, b + k * (2048 / 16), idesc_o, 1u);
                         if (!more) umma_commit(o_full(t));
                         else scores(t, ks);
@@ -376,16 +380,16 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     for (int c = 0; c < kManyKeys; ++c)
                         if (c >= seen) x[c] = off;
                 }
-                // The weights of half the keys, relative to the maximum so far, and meanwhile the
+                // The weights of the first keys, relative to the maximum so far, and meanwhile the
                 // largest score (the smallest, times a scale below zero): only where that has
                 // outgrown the maximum, the weights are formed again.
                 uint32_t p[kManyKeys / 2];
                 float2 sum[2];
-                auto weigh = [&](int half) {
+                auto weigh = [&](int from, int until) {
                     const float b = m == neg_inf() ? 0.0f : -m;
                     const float2 base = make_float2(b, b), scale = make_float2(g.scale2, g.scale2);
 #pragma unroll
-                    for (int i = half * 64; i < half * 64 + 64; i += 2) {
+                    for (int i = from; i < until; i += 2) {
                         const float2 y = __ffma2_rn(make_float2(x[i], x[i + 1]), scale, base);
                         const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
                         sum[(i / 2) % 2] = __fadd2_rn(sum[(i / 2) % 2], e);
@@ -393,7 +397,7 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                 };
                 sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-                weigh(0);
+                weigh(0, kFirstKeys);
                 float top;
                 if (g.scale2 >= 0.0f) {
                     float a = max3(x[0], x[1], x[2]), b = max3(x[3], x[4], x[5]);
@@ -434,17 +438,18 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         }
                     }
                     sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-                    weigh(0);
+                    weigh(0, kFirstKeys);
                 }
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (half == 1) weigh(1);
-                    tmem_st16(s_at + half * 32, p + half * 32);
-                    tmem_st16(s_at + half * 32 + 16, p + half * 32 + 16);
+                for (int part = 0; part < 2; ++part) {
+                    if (part == 1) weigh(kFirstKeys, kManyKeys);
+#pragma unroll
+                    for (int c = part == 0 ? 0 : kFirstKeys; c < (part == 0 ? kFirstKeys : kManyKeys); c += 32)
+                        tmem_st16(s_at + c / 2, p + c / 2);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full(t, half));   // half the keys: their products may begin
+                    if (lane == 0) mbar_arrive(p_full(t, part));   // the products of these keys may begin
                 }
                 sum[0] = __fadd2_rn(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;

@@ -143,11 +143,30 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
     if (g.limits != nullptr && all_runs > 0) {
         for (int i = t; i < all_runs; i += T) run_keys[i] = 0;
         __syncthreads();
-        for (int s = t; s < g.S; s += T) {
-            if (s < first_of[0] || s >= first_of[g.groups]) continue;
-            const int group = last_at_most(first_of, g.groups, s), first = first_of[group];
-            if (!few_group(first_of[group + 1] - first))
-                atomicMax(run_keys + run_of[group] + (s - first) / run, keys_seen(group, s));
+        // (four limits on their way at a time; a warp's queries are of one run as a rule, and one lane
+        // answers for those that are)
+        for (int s0 = 0; s0 < g.S; s0 += 4 * T) {
+            int seen[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) seen[i] = s0 + i * T + t < g.S ? g.limits[s0 + i * T + t] : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int s = s0 + i * T + t;
+                int r = -1, keys = 0;
+                if (s < g.S && s >= first_of[0] && s < first_of[g.groups]) {
+                    const int group = last_at_most(first_of, g.groups, s), first = first_of[group];
+                    if (!few_group(first_of[group + 1] - first)) {
+                        r = run_of[group] + (s - first) / run;
+                        keys = max(0, min(group_len(group), seen[i]));
+                    }
+                }
+                if (__match_any_sync(~0u, r) == ~0u) {
+                    keys = __reduce_max_sync(~0u, keys);
+                    if (r >= 0 && (t & 31) == 0) atomicMax(run_keys + r, keys);
+                } else if (r >= 0) {
+                    atomicMax(run_keys + r, keys);
+                }
+            }
         }
         __syncthreads();
     }
@@ -237,7 +256,18 @@ struct AttnParts {
     const float *at;       // the first part's row
     const float2 *stats;
     int step;              // rows from a part to the next (but from the first to the second, half of it)
-    bool final;            // already in the output
+
+    __device__ __forceinline__ int64_t place(int c) const {
+        return c == 0 ? 0 : static_cast<int64_t>(2 * c - 1) * (step >> 1);
+    }
+    __device__ __forceinline__ AttnParts from(int lane) const {   // a lane's, for all
+        AttnParts p;
+        p.count = __shfl_sync(~0u, count, lane);
+        p.at = reinterpret_cast<const float *>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(at), lane));
+        p.stats = reinterpret_cast<const float2 *>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(stats), lane));
+        p.step = __shfl_sync(~0u, step, lane);
+        return p;
+    }
 };
 
 __device__ __forceinline__ AttnParts parts_of(const AttnArgs &g, const AttnPlace &q, const AttnCounts &n, int64_t whole,
@@ -254,7 +284,6 @@ __device__ __forceinline__ AttnParts parts_of(const AttnArgs &g, const AttnPlace
     const int64_t u0 = q.start + static_cast<int64_t>(seg) * (q.units + cost) + cost;
     const int c0 = owner_of(n.units, ctas, u0), c1 = owner_of(n.units, ctas, u0 + q.units - 1);
     p.count = c1 - c0 + 1;
-    p.final = p.count == 1 && g.alone;
     int64_t at = whole;
     if (p.count == 1) {
         p.at = g.whole[kind];
@@ -270,91 +299,181 @@ __device__ __forceinline__ AttnParts parts_of(const AttnArgs &g, const AttnPlace
     return p;
 }
 
-// A warp takes `each` rows (query, query head): which of them have parts to join is looked at
-// a lane each, then the warp joins one after another.
+// The parts of R rows added up by a warp: the maxima and sums a part a lane, the values V to a
+// lane.  Everything of a kind is on its way at once; the parts come in the order of their index.
+template <typename C, int D, int R>
+struct JoinedRows {
+    static constexpr int V = D / 32;
+    float o[R][V], m[R], l[R];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = neg_inf();
+            l[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[r][i] = 0.0f;
+        }
+    }
+    // part(c): the first row's values and statistics in part c; row r lies r * row_step rows on
+    template <typename F>
+    __device__ __forceinline__ void add(int count, int row_step, int lane, F part) {
+        for (int c0 = 0; c0 < count; c0 += 32) {
+            const int n = min(32, count - c0);
+            const float *at = nullptr;
+            const float2 *stats = nullptr;
+            if (lane < n) part(c0 + lane, at, stats);
+            float2 st[R];
+            float w[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                st[r] = lane < n ? __ldcg(stats + r * row_step) : make_float2(neg_inf(), 0.0f);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float top = st[r].x;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                const float nm = fmaxf(m[r], top), base = nm == neg_inf() ? 0.0f : nm;
+                const float old = exp2_fast(m[r] - base);
+                w[r] = exp2_fast(st[r].x - base);
+                float sum = lane < n ? st[r].y * w[r] : 0.0f;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+                m[r] = nm;
+                l[r] = l[r] * old + sum;
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[r][i] *= old;
+            }
+#pragma unroll(R == 1 ? 8 : 2)
+            for (int j = 0; j < n; ++j) {
+                const float *src = reinterpret_cast<const float *>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(at), j)) + lane * V;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float f = __shfl_sync(~0u, w[r], j);
+                    if constexpr (V == 4) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + static_cast<int64_t>(r) * row_step * D));
+                        o[r][0] = fmaf(f, v.x, o[r][0]), o[r][1] = fmaf(f, v.y, o[r][1]);
+                        o[r][2] = fmaf(f, v.z, o[r][2]), o[r][3] = fmaf(f, v.w, o[r][3]);
+                    } else {
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + static_cast<int64_t>(r) * row_step * D));
+                        o[r][0] = fmaf(f, v.x, o[r][0]), o[r][1] = fmaf(f, v.y, o[r][1]);
+                    }
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void put(const AttnArgs &g, int which, int64_t row, int lane) const {
+        if (!q4_in_bounds(row >= 0 && row < static_cast<int64_t>(g.S) * g.Hq, g.bounds)) return;
+        const float f = l[which] != 0.0f ? 1.0f / l[which] : 0.0f;   // (no key: zeros)
+        if (lane == 0 && g.lse != nullptr) g.lse[row] = lse_of(m[which], l[which]);
+        const int64_t to = row * D + lane * V;
+        const float *v = o[which];
+        if (g.out_f32) {
+            float *p = static_cast<float *>(g.out) + to;
+#pragma unroll
+            for (int i = 0; i < V; i += 2) *reinterpret_cast<float2 *>(p + i) = make_float2(v[i] * f, v[i + 1] * f);
+        } else {
+            uint32_t *p = reinterpret_cast<uint32_t *>(static_cast<C *>(g.out) + to);
+#pragma unroll
+            for (int i = 0; i < V; i += 2) p[i / 2] = pack2<C>(v[i] * f, v[i + 1] * f);
+        }
+    }
+};
+
+// Calls with both kinds of segments: every row has parts to join.  A warp takes `each` rows
+// (query, query head), where their parts are is looked up a lane each.
 template <typename C, int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs g, int each) {
-    constexpr int V = D / 32;
     const int lane = threadIdx.x & 31;
     const int64_t rows = static_cast<int64_t>(g.S) * g.Hq;
     const int64_t first = (static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5)) * each;
     wait_prior_grid();
     allow_next_grid();
     AttnParts a = {}, b = {};   // shared, own
-    bool todo = false;
     if (lane < each && first + lane < rows) {
         const int s = static_cast<int>((first + lane) / g.Hq), head = static_cast<int>((first + lane) - static_cast<int64_t>(s) * g.Hq);
-        AttnPlace qa = {}, qb = {};
         const AttnCounts many = *g.many, few = *g.few;
-        if (g.groups > 0) qa = g.places[s];
-        if (g.own_lens != nullptr) qb = g.places[g.S + s];
+        const AttnPlace qa = g.places[s], qb = g.places[g.S + s];
         a = parts_of(g, qa, qa.many != 0 ? many : few, first + lane, head, 0);
         b = parts_of(g, qb, few, first + lane, head, 1);
-        todo = !(a.final || b.final);
     }
-    unsigned left = __ballot_sync(~0u, todo);
-    while (left != 0) {
-        const int from = __ffs(left) - 1;
-        left &= left - 1;
-        const int64_t row = first + from;
-        float o[V], m = neg_inf(), l = 0.0f;
+    for (int i = 0; i < each && first + i < rows; ++i) {
+        const AttnParts pa = a.from(i), pb = b.from(i);
+        JoinedRows<C, D, 1> row;
+        row.clear();
+        row.add(pa.count + pb.count, 0, lane, [&](int c, const float *&at, const float2 *&stats) {
+            const AttnParts &p = c < pa.count ? pa : pb;
+            const int64_t place = p.place(c < pa.count ? c : c - pa.count);
+            at = p.at + place * D;
+            stats = p.stats + place;
+        });
+        row.put(g, 0, first + i, lane);
+    }
+}
+
+// Calls with one kind of segments: whole ones are in the output already, and what is left are
+// the segments that the border between two CTAs' shares cuts (each dealt with at the first
+// border that does), and the queries without a key.
+constexpr int kBorderRows = 8;   // CTAs of the rows of a border of the kernel for many rows (few rows: one)
+
+template <typename C, int D, int KEYS, int COST, bool FEW>
+__device__ __forceinline__ void join_border(const AttnArgs &g, int c, int part, int lane, int warp) {
+    const AttnCounts n = FEW ? *g.few : *g.many;
+    const int ctas = ctas_of(n.units, FEW ? g.few_ctas : g.many_ctas);
+    if (c + 1 >= ctas) return;
+    const int64_t *start = FEW ? g.few_start : g.many_start;
+    const int64_t border = units_before(n.units, ctas, c + 1);
+    const int entry = entry_at(start, n.entries, border, lane);
+    const AttnEntry e = FEW ? g.few_entries[entry] : g.many_entries[entry];
+    const int units = (e.keys + KEYS - 1) / KEYS, each = units + COST;
+    const int seg = static_cast<int>(quotient(border - start[entry], each));
+    const int64_t u0 = start[entry] + static_cast<int64_t>(seg) * each + COST;   // its first unit
+    const int count = owner_of(n.units, ctas, u0 + units - 1) - c + 1;
+    if (owner_of(n.units, ctas, u0) != c || count < 2) return;
+    const int tiles = FEW ? (e.queries * g.G + kFewRows - 1) / kFewRows : 1;
+    const int kv = seg / tiles, tile = seg - kv * tiles, rows = FEW ? kFewRows : 128 * kManyTiles;
+    const int per = g.tile_queries * g.G, all = e.queries * g.G;
+    const float *base = (FEW ? g.few_part : g.many_part) + static_cast<int64_t>(2 * c + 1) * rows * D;
+    const float2 *stats = (FEW ? g.few_stats : g.many_stats) + static_cast<int64_t>(2 * c + 1) * rows;
+    // a warp's rows, four at a time: those of no query are added up as well, but not put
+    constexpr int kWarps = kJoinThreads / 32, kApart = (FEW ? 1 : kBorderRows) * kWarps, R = FEW ? kFewRows / kWarps : 4;
+    AttnParts p = {count, nullptr, nullptr, 2 * rows};
+    for (int r0 = part * kWarps + warp; r0 < rows; r0 += R * kApart) {
+        JoinedRows<C, D, R> out;
+        out.clear();
+        out.add(count, kApart, lane, [&](int i, const float *&at, const float2 *&st) {
+            at = base + (p.place(i) + r0) * D;
+            st = stats + p.place(i) + r0;
+        });
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = 0.0f;
-        auto add = [&](const AttnParts &mine) {
-            const int count = __shfl_sync(~0u, mine.count, from);
-            const float *at = reinterpret_cast<const float *>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine.at), from));
-            const float2 *stats =
-                reinterpret_cast<const float2 *>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine.stats), from));
-            const int step = __shfl_sync(~0u, mine.step, from);
-            auto place = [&](int c) { return c == 0 ? 0 : static_cast<int64_t>(2 * c - 1) * (step >> 1); };
-            for (int c0 = 0; c0 < count; c0 += 32) {
-                const int n = min(32, count - c0);
-                // a part a lane: its maximum and sum, then its weight among these
-                const int c = c0 + lane;
-                float2 st = make_float2(neg_inf(), 0.0f);
-                if (lane < n) st = __ldcg(stats + place(c));
-                float top = st.x;
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-                const float nm = fmaxf(m, top), base = nm == neg_inf() ? 0.0f : nm;
-                const float old = exp2_fast(m - base), w = exp2_fast(st.x - base);
-                float sum = st.y * w;
-                if (lane >= n) sum = 0.0f;
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-                m = nm;
-                l = l * old + sum;
-#pragma unroll
-                for (int i = 0; i < V; ++i) o[i] *= old;
-#pragma unroll 8
-                for (int j = 0; j < n; ++j) {
-                    const float f = __shfl_sync(~0u, w, j);
-                    const float *src = at + place(c0 + j) * D + lane * V;
-                    if constexpr (V == 4) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                        o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]);
-                        o[2] = fmaf(f, v.z, o[2]), o[3] = fmaf(f, v.w, o[3]);
-                    } else {
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                        o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]);
-                    }
-                }
-            }
-        };
-        add(a);
-        add(b);
-        const float r = l != 0.0f ? 1.0f / l : 0.0f;   // (no key: zeros)
-        if (!q4_in_bounds(row < rows, g.bounds)) continue;
-        if (lane == 0 && g.lse != nullptr) g.lse[row] = lse_of(m, l);
-        const int64_t to = row * D + lane * V;
-        if (g.out_f32) {
-            float *p = static_cast<float *>(g.out) + to;
-#pragma unroll
-            for (int i = 0; i < V; i += 2) *reinterpret_cast<float2 *>(p + i) = make_float2(o[i] * r, o[i + 1] * r);
-        } else {
-            uint32_t *p = reinterpret_cast<uint32_t *>(static_cast<C *>(g.out) + to);
-#pragma unroll
-            for (int i = 0; i < V; i += 2) p[i / 2] = pack2<C>(o[i] * r, o[i + 1] * r);
+        for (int i = 0; i < R; ++i) {
+            const int r = r0 + i * kApart;   // row of the parts: which query and head
+            const int row = FEW ? tile * kFewRows + r : r / 128 * per + r % 128;
+            if (row >= all || (!FEW && r % 128 >= per)) continue;
+            out.put(g, i, static_cast<int64_t>(e.first + row / g.G) * g.Hq + kv * g.G + row % g.G, lane);
+        }
+    }
+}
+
+template <typename C, int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_borders_kernel(const AttnArgs g, int many_borders) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    wait_prior_grid();
+    allow_next_grid();
+    const int c = blockIdx.x, many = many_borders * kBorderRows;
+    if (c < many) join_border<C, D, kManyKeys, kManyCost, false>(g, c / kBorderRows, c % kBorderRows, lane, warp);
+    else join_border<C, D, kFewKeys, kFewCost, true>(g, c - many, 0, lane, warp);
+    // queries without a key: a warp looks at 32 at a time
+    const AttnPlace *places = g.groups > 0 ? g.places : g.places + g.S;
+    const int warps = gridDim.x * (kJoinThreads / 32);
+    for (int s0 = (blockIdx.x * (kJoinThreads / 32) + warp) * 32; s0 < g.S; s0 += warps * 32) {
+        unsigned empty = __ballot_sync(~0u, s0 + lane < g.S && places[min(s0 + lane, g.S - 1)].units == 0);
+        while (empty != 0) {
+            const int s = s0 + __ffs(empty) - 1;
+            empty &= empty - 1;
+            JoinedRows<C, D, 1> none;
+            none.clear();
+            for (int h = 0; h < g.Hq; ++h) none.put(g, 0, static_cast<int64_t>(s) * g.Hq + h, lane);
         }
     }
 }
@@ -453,7 +572,8 @@ int launch_attn(const q4_prefix_attn_t &a, const AttnArgs &g, cudaStream_t strea
         if (st != Q4_OK) return st;
     }
     // (no own segments and one group: all its queries have more than 16 rows, or all are few)
-    if (a.own_lens != nullptr || g.many_ctas == 0 || a.groups > 1 || a.group_offsets != nullptr) {
+    const bool few = a.own_lens != nullptr || g.many_ctas == 0 || a.groups > 1 || a.group_offsets != nullptr;
+    if (few) {
         using F = FewAttn<D>;
         static_assert(2 * (F::smem() + 1024) <= 228 * 1024, "two CTAs of an SM");
         static std::atomic<bool> configured[64];
@@ -461,6 +581,11 @@ int launch_attn(const q4_prefix_attn_t &a, const AttnArgs &g, cudaStream_t strea
         st = launch_overlappable(attn_few_kernel<C, D>, dim3(static_cast<unsigned>(g.few_ctas)), dim3(F::kThreads),
                                  F::smem(), stream, true, map_k, map_v, g);
         if (st != Q4_OK) return st;
+    }
+    if (g.alone) {
+        const int borders = g.many_ctas * kBorderRows + (few ? g.few_ctas : 0);
+        return launch_overlappable(attn_borders_kernel<C, D>, dim3(static_cast<unsigned>(borders)), dim3(kJoinThreads), 0,
+                                   stream, true, g, g.many_ctas);
     }
     // rows of a warp: one where there are few, so that the parts are read by many warps
     const int64_t rows = static_cast<int64_t>(a.S) * a.Hq;
