@@ -17,7 +17,10 @@
 // side), so a rotation never leaves a lane, or, beyond rot, single vectors.  The mean is a
 // sum over the L lanes by shuffles.
 //
-// Bound: the bytes of the rows and of the outputs for prompts; latency for decoding.
+// Bound: latency for decoding (4.0 us for 4 tokens); for prompts the chain from a row's load to
+// its store with what an SM's CTAs have in flight: 25.4 us for the 101 MB of 4096 tokens, 4.0
+// TB/s, 0.59 of measured.  Heads in a loop with the cosines and weights in registers (27 us),
+// and four tokens to a CTA with the next one's rows on their way (32 us), gained nothing.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -93,22 +96,56 @@ __device__ __forceinline__ void store_vec(C *p, const float *in) {
     if constexpr (V == 1) {
         *p = narrow<C>(in[0]);
     } else {
-        C v[8];
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = narrow<C>(in[i]);
-        *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(v);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (std::is_same<C, __half>::value)
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(in[2 * i + 1]), "f"(in[2 * i]));
+            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(in[2 * i + 1]), "f"(in[2 * i]));
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
-constexpr int kRopeThreads = 384;
+// v * r * gamma
+template <int V>
+__device__ __forceinline__ void scale_vec(float *v, float r, const float *gamma) {
+    if constexpr (V == 1) {
+        v[0] = v[0] * r * gamma[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 w = __ldg(reinterpret_cast<const float4 *>(gamma + i));
+            const float2 rr = make_float2(r, r);
+            const float2 f = __fmul2_rn(__fmul2_rn(make_float2(v[i], v[i + 1]), rr), make_float2(w.x, w.y));
+            const float2 h = __fmul2_rn(__fmul2_rn(make_float2(v[i + 2], v[i + 3]), rr), make_float2(w.z, w.w));
+            v[i] = f.x, v[i + 1] = f.y, v[i + 2] = h.x, v[i + 3] = h.y;
+        }
+    }
+}
+
+// Two pairs (x, y) turned, the first and the second of each.
+__device__ __forceinline__ void turn2(float &x0, float &x1, float &y0, float &y1, const float *c, const float *s) {
+    const float2 cc = *reinterpret_cast<const float2 *>(c), ss = *reinterpret_cast<const float2 *>(s);
+    const float2 x = make_float2(x0, x1), y = make_float2(y0, y1);
+    const float2 nx = __ffma2_rn(x, cc, __fmul2_rn(y, make_float2(-ss.x, -ss.y)));
+    const float2 ny = __ffma2_rn(x, ss, __fmul2_rn(y, cc));
+    x0 = nx.x, x1 = nx.y;
+    y0 = ny.x, y1 = ny.y;
+}
+
+// Threads of a CTA at most; of a call of many tokens (kManyTokens to an SM) fewer, which have
+// their heads in turn: 4096 tokens of 32 + 2 x 8 heads (101 MB) 28.2 us with 384, 25.4 with 128;
+// 4 tokens 4.0 and 5.5.
+constexpr int kRopeThreads = 384, kPromptThreads = 128, kManyTokens = 8;
 
 }  // namespace
 
 // T: type of q, k, v; C: of the cache and q_out; V features an access, L lanes a head, NJ jobs
 // a lane at most.
 template <typename T, typename C, int V, int L, int NJ>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const q4_rope_append_t g, unsigned int *bounds) {
-    __shared__ float cs[kMaxHeadD / 2], sn[kMaxHeadD / 2];
+__global__ void __launch_bounds__(kRopeThreads, V == 1 ? 2 : 4) rope_append_kernel(const q4_rope_append_t g, unsigned int *bounds) {
+    __shared__ __align__(16) float cs[kMaxHeadD / 2], sn[kMaxHeadD / 2];
     const int t = blockIdx.x;
     const int D = g.cache.D, half = g.rot / 2;
     const bool pairs_apart = g.layout == Q4_ROPE_HALF;
@@ -121,6 +158,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const q4_rope
     };
     wait_prior_grid();
     allow_next_grid();
+    const int position = g.rot > 0 ? g.positions[t] : 0;
+    const int slot = g.slots != nullptr ? g.slots[t] : t;   // (on its way with the heads)
     bool turned = false;   // the cosines and sines are in shared memory
     for (int h0 = 0; h0 < heads; h0 += per) {
         const int h = h0 + sub;
@@ -148,29 +187,40 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const q4_rope
         }
         if (!turned) {
             for (int i = threadIdx.x; i < half; i += blockDim.x)
-                cos_sin(g.positions[t], g.inv_freq[i], g.scale, cs[i], sn[i]);
+                cos_sin(position, g.inv_freq[i], g.scale, cs[i], sn[i]);
             __syncthreads();
             turned = true;
         }
         const float *gamma = kind == 0 ? g.q_gamma : kind == 1 ? g.k_gamma : nullptr;
-        float ss = 0.0f;
+        float r = 1.0f;
+        if (g.q_gamma != nullptr || g.k_gamma != nullptr) {   // (the sums are of all lanes)
+            float ss = 0.0f;
+            float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int n = 0; n < NJ; ++n)
+            for (int n = 0; n < NJ; ++n)
 #pragma unroll
-            for (int v = 0; v < V; ++v) ss = fmaf(a[n][v], a[n][v], fmaf(b[n][v], b[n][v], ss));
+                for (int v = 0; v < V; v += V == 1 ? 1 : 2) {
+                    if constexpr (V == 1) {
+                        ss = fmaf(a[n][v], a[n][v], fmaf(b[n][v], b[n][v], ss));
+                    } else {
+                        const float2 x = make_float2(a[n][v], a[n][v + 1]), y = make_float2(b[n][v], b[n][v + 1]);
+                        sq = __ffma2_rn(x, x, __ffma2_rn(y, y, sq));
+                    }
+                }
+            ss += sq.x + sq.y;
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-        const float r = 1.0f / sqrtf(ss / static_cast<float>(D) + g.eps);
+            for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+            r = rsqrtf(ss / static_cast<float>(D) + g.eps);   // (off by 2^-22, the rounding to come by 2^-11)
+        }
         if (!have) continue;   // (lanes that skip the stores meet the others at the next turn's sums)
         C *dst;
         if (kind == 0) {
             dst = static_cast<C *>(g.q_out) + (static_cast<int64_t>(t) * g.Hq + at) * D;
         } else {
-            const int64_t slot = g.slots != nullptr ? g.slots[t] : t;
-            const int64_t page = slot >= 0 ? slot / g.cache.page : -1;
+            const int page = slot >= 0 ? slot / g.cache.page : -1;
             if (page < 0 || page >= g.cache.pages) continue;
-            dst = static_cast<C *>(kind == 1 ? g.cache.k : g.cache.v) + page * g.cache.page_stride +
-                  at * g.cache.head_stride + (slot - page * g.cache.page) * g.cache.row_stride;
+            dst = static_cast<C *>(kind == 1 ? g.cache.k : g.cache.v) + static_cast<int64_t>(page) * g.cache.page_stride +
+                  at * g.cache.head_stride + static_cast<int64_t>(slot - page * g.cache.page) * g.cache.row_stride;
         }
 #pragma unroll
         for (int n = 0; n < NJ; ++n) {
@@ -180,34 +230,25 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const q4_rope
             const int c = pair ? (pairs_apart ? j * V : 2 * j * V) : g.rot + (j - pairs) * V;
             const int c2 = c + (pairs_apart ? half : V);
             if (gamma != nullptr) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    a[n][v] = a[n][v] * r * gamma[c + v];
-                    if (pair) b[n][v] = b[n][v] * r * gamma[c2 + v];
-                }
+                scale_vec<V>(a[n], r, gamma + c);
+                if (pair) scale_vec<V>(b[n], r, gamma + c2);
             }
             if (pair && kind != 2) {
-                if (pairs_apart) {
+                if constexpr (V == 1) {
+                    const int at = pairs_apart ? c : c / 2;
+                    const float x = a[n][0], y = b[n][0];
+                    a[n][0] = cs[at] * x - sn[at] * y;
+                    b[n][0] = sn[at] * x + cs[at] * y;
+                } else if (pairs_apart) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float x = a[n][v], y = b[n][v], cc = cs[c + v], s = sn[c + v];
-                        a[n][v] = cc * x - s * y;
-                        b[n][v] = s * x + cc * y;
-                    }
-                } else if constexpr (V > 1) {
-#pragma unroll
-                    for (int v = 0; v < V; v += 2) {
-                        float x = a[n][v], y = a[n][v + 1], cc = cs[(c + v) / 2], s = sn[(c + v) / 2];
-                        a[n][v] = cc * x - s * y;
-                        a[n][v + 1] = s * x + cc * y;
-                        x = b[n][v], y = b[n][v + 1], cc = cs[(c2 + v) / 2], s = sn[(c2 + v) / 2];
-                        b[n][v] = cc * x - s * y;
-                        b[n][v + 1] = s * x + cc * y;
-                    }
+                    for (int v = 0; v < V; v += 2)
+                        turn2(a[n][v], a[n][v + 1], b[n][v], b[n][v + 1], cs + j * V + v, sn + j * V + v);
                 } else {
-                    const float x = a[n][0], y = b[n][0], cc = cs[c / 2], s = sn[c / 2];
-                    a[n][0] = cc * x - s * y;
-                    b[n][0] = s * x + cc * y;
+#pragma unroll
+                    for (int v = 0; v < V; v += 4) {
+                        turn2(a[n][v], a[n][v + 2], a[n][v + 1], a[n][v + 3], cs + j * V + v / 2, sn + j * V + v / 2);
+                        turn2(b[n][v], b[n][v + 2], b[n][v + 1], b[n][v + 3], cs + j * V + (V + v) / 2, sn + j * V + (V + v) / 2);
+                    }
                 }
             }
             if (ib(t, g.T, c, dst + c, sizeof(C))) store_vec<C, V>(dst + c, a[n]);
@@ -220,16 +261,17 @@ template <typename T, typename C>
 static int launch_rope_of(const q4_rope_append_t &a, cudaStream_t stream) {
     const int D = a.cache.D, half = a.rot / 2;
     const int heads = a.Hq + (a.k != nullptr ? 2 * a.cache.heads : 0);
-    // vectors of 8 features where every row, head, pair and page starts on 16 bytes
+    // vectors of 8 features where every row, head, pair and page and the norm weights start on 16 bytes
     auto rows = [&](const void *p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; };
     const bool wide = D % 8 == 0 && a.rot % 16 == 0 && (a.layout != Q4_ROPE_HALF || half % 8 == 0) &&
                       rows(a.q, a.q_stride) && rows(a.k, a.k_stride) && rows(a.v, a.v_stride) && aligned(a.q_out, 16) &&
                       rows(a.cache.k, a.cache.page_stride) && rows(a.cache.v, a.cache.head_stride) &&
-                      a.cache.row_stride % 8 == 0;
+                      a.cache.row_stride % 8 == 0 && aligned(a.q_gamma, 16) && aligned(a.k_gamma, 16);
     auto launch = [&](auto kernel, int L) {
         const int need = (heads * L + 31) / 32 * 32;
-        // as few turns as the largest block allows, and no more threads than those turns need
-        const int turns = (need + kRopeThreads - 1) / kRopeThreads;
+        // as few turns as the block allows, and no more threads than those turns need
+        const int most = a.T >= kManyTokens * device_info().sms ? kPromptThreads : kRopeThreads;
+        const int turns = (need + most - 1) / most;
         const unsigned threads = static_cast<unsigned>((need / turns + 31) / 32 * 32);
         return launch_overlappable(kernel, dim3(static_cast<unsigned>(a.T)), dim3(threads), 0, stream,
                                    call_options().overlap, a, bounds_counter());
