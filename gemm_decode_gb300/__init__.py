@@ -718,10 +718,21 @@ def _device(t, name):
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name}: a CUDA tensor expected, got {t.device}")
-    import torch
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{name}: on CUDA device {dev}, which is not the current one")
     return dev
+
+
+_raw_device = None
+
+
+def _current_device():
+    """The current CUDA device's index (without torch's own wrapper where that can be left out)."""
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _raw_device()
 
 
 def _half_dtype(t, name):

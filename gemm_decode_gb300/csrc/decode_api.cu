@@ -161,7 +161,7 @@ int q4_prefix_attn_run(const q4_prefix_attn_t *args, const q4_run_options_t *opt
     const q4_kv_cache_t &c = g.cache;
     if ((st = cache_shape(c)) != Q4_OK) return st;
     if ((st = attn_shape(g.S, g.groups, g.Hq, c.heads, c.D)) != Q4_OK) return st;
-    if ((g.out_dtype != c.dtype && g.out_dtype != Q4_F32) || !finite(g.scale) || g.max_shared_pages < 0 ||
+    if ((g.out_dtype != c.dtype && g.out_dtype != Q4_F32) || !(std::fabs(g.scale) <= 1e38f) || g.max_shared_pages < 0 ||
         g.max_own_pages < 0)
         return Q4_ERR_INVALID_ARG;
     const bool own = g.own_pages != nullptr || g.own_lens != nullptr;

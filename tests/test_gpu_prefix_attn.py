@@ -283,3 +283,24 @@ def test_a_cache_beyond_32_bits(torch):
                                  small["own_pages"], p["own_lens"].cpu(), D ** -0.5, torch.bfloat16)
     ref.within(out, o, 1.01 * bo + ref.rounding(o, torch.bfloat16), "out")
     ref.within(lse, l, bl, "lse")
+
+
+def test_bounded_waits_report_a_timeout_and_the_next_call_is_right(torch):
+    """A bound of 0: each wait that is not satisfied at once gives up, the kernels end, and the
+    status says so.  (Groups of both kinds: both kernels.)"""
+    p = problem(torch, [70, 2], [3000, 500], [200] * 72, 8, 2, 128, 16, torch.bfloat16)
+    run(torch, p, wait_timeout_ns=0)
+    assert q4.q4gemv_device_status() == q4.Q4_ERR_TIMEOUT
+    assert q4.q4gemv_device_status() == q4.Q4_OK
+    check(torch, p)
+
+
+def test_a_prompt_and_a_search_in_one_workspace(torch):
+    """Calls of other sizes and kinds one after another in the largest one's workspace."""
+    a = problem(torch, [300], [300], None, 8, 2, 128, 16, torch.bfloat16)
+    a["limits"] = (1 + torch.arange(300, device="cuda")).to(torch.int32)
+    b = problem(torch, [4, 4], [700, 90], [33] * 8, 8, 2, 128, 16, torch.bfloat16)
+    c = problem(torch, [9], None, [1000] * 9, 8, 2, 64, 32, torch.float16)
+    ws = torch.full((q4.q4_prefix_attn_workspace(300, 2, 8, 2, 128),), 255, device="cuda", dtype=torch.uint8)
+    for p in (a, b, c, a, c, b):
+        check(torch, p, ws=ws, flags=q4.Q4_RUN_OVERLAPPED)
