@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 __all__ = [
@@ -191,15 +192,16 @@ def lib() -> ctypes.CDLL:
                                          _i32, _vp, _i64, _opt, _vp]
             L.q4_block_norm_run.argtypes = [ctypes.POINTER(_BlockNorm), _opt, _vp]
             L.q4moe_block_run.argtypes = [ctypes.POINTER(_MoeBlock), _opt, _vp]
-            L.q4_rope_append_run.argtypes = [ctypes.POINTER(_RopeAppend), _opt, _vp]
+            # (the structures as bytes)
+            L.q4_rope_append_run.argtypes = [_vp, _opt, _vp]
             _f64 = ctypes.c_double
             L.q4_rope_frequencies.argtypes = [ctypes.POINTER(ctypes.c_float), _i32, _f64, _i32, _f64, _f64, _f64, _f64]
             L.q4_prefix_attn_workspace.argtypes = [_i32] * 5
-            L.q4_prefix_attn_run.argtypes = [ctypes.POINTER(_PrefixAttn), _opt, _vp]
+            L.q4_prefix_attn_run.argtypes = [_vp, _opt, _vp]
             L.q4_beam_step_workspace.argtypes = [_i32, _i32, _i32, _i64]
             L.q4_beam_step_run.argtypes = [_vp, _i64, _vp, _vp, _i32, _i32, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp,
                                            _i64, _opt, _vp]
-            L.q4_beam_reorder_run.argtypes = [ctypes.POINTER(_BeamReorder), _opt, _vp]
+            L.q4_beam_reorder_run.argtypes = [_vp, _opt, _vp]
             for f in ("q4_prefix_attn_workspace", "q4_beam_step_workspace"):
                 getattr(L, f).restype = _i64
             for f in ("q4_rope_append_run", "q4_rope_frequencies", "q4_prefix_attn_run", "q4_beam_step_run",
@@ -697,18 +699,27 @@ def q4moe_block_run(up, down, logits, a, x, out, out_norm, ids, route_weights, w
 
 
 # ------------------------------------------------- several continuations of one prompt
+#
+# What these calls do on the GPU may take no longer than their arguments' way there, so the
+# structures are packed in one go (a ctypes structure of 30 fields takes 1.4 us, this 0.2) and
+# the checks of a call are one expression, whose parts are told apart only where it fails.
+
+_ROPE = struct.Struct("@5i2f3P3q6P2P4i4q")
+_ATTN = struct.Struct("@6if P q 2P4i4q 9P q")
+_REORDER = struct.Struct("@6i6q7P")
+
 
 def _on(dev, t, name, dtype):
-    """Address of a contiguous tensor of the given type on device `dev` (None passes through)."""
+    """Address of a contiguous tensor of the given type on device `dev` (0 for None)."""
     if t is None:
-        return None
+        return 0
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor is required (got strides {tuple(t.stride())})")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: a tensor on CUDA device {dev} expected, got {t.device}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: a tensor on CUDA device {dev} expected, got {t.device}")
 
 
 def _device(t, name):
@@ -745,22 +756,26 @@ def _half_dtype(t, name):
 
 
 def _cache(dev, k, v):
-    """The paged cache of two pools [pages, kv heads, tokens of a page, features]."""
-    pages, heads, page, D = k.shape
-    stride = k.stride()
-    _need(k.shape == v.shape and stride == v.stride() and k.dtype is v.dtype and stride[3] == 1 and
-          k.get_device() == dev and v.get_device() == dev,
-          "k_cache, v_cache: the same shape, strides, type and device, and features side by side")
-    return _KvCache(k.data_ptr(), v.data_ptr(), _half_dtype(k, "k_cache"), heads, D, page, pages, stride[0], stride[1],
-                    stride[2])
+    """The paged cache of two pools [pages, kv heads, tokens of a page, features]: the fields of
+    q4_kv_cache_t."""
+    shape, stride = k.shape, k.stride()
+    dtype = k.dtype
+    if not (len(shape) == 4 and v.shape == shape and v.stride() == stride and v.dtype is dtype and
+            (stride[3] == 1 or shape[3] == 1) and k.get_device() == dev and v.get_device() == dev):
+        raise ValueError("k_cache, v_cache: [pages, heads, tokens of a page, features] of the same shape, strides, type "
+                         "and device, with features side by side, expected")
+    pages, heads, page, D = shape
+    return (k.data_ptr(), v.data_ptr(), Q4_BF16 if dtype is _Types.bf16 else _half_dtype(k, "k_cache"), heads, D, page,
+            pages, stride[0], stride[1], stride[2])
 
 
-def _heads(dev, t, name, T, D, dtype):
-    """(address, elements from one token to the next) of [T, heads, D] with the heads of a token side by side."""
-    s, n = t.stride(), t.shape
-    _need(len(n) == 3 and n[0] == T and n[2] == D and (s[2] == 1 or D == 1) and (s[1] == D or n[1] == 1) and
-          t.dtype is dtype and t.get_device() == dev,
-          f"{name}: [tokens, heads, {D}] of {dtype} with the heads of a token side by side expected")
+def _heads(dev, t, name, T, H, D, dtype):
+    """(address, elements from one token to the next) of [T, H, D] with the heads of a token side by side."""
+    s = t.stride()
+    if not (t.shape == (T, H, D) and (s[2] == 1 or D == 1) and (s[1] == D or H == 1) and t.dtype is dtype and
+            t.get_device() == dev):
+        raise ValueError(f"{name}: [{T}, {H}, {D}] of {dtype} on CUDA device {dev} with the heads of a token side by side "
+                         f"expected, got {tuple(t.shape)} of {t.dtype} on {t.device} with strides {tuple(s)}")
     return t.data_ptr(), s[0]
 
 
@@ -773,26 +788,29 @@ def q4_rope_append_run(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, sl
     2 len(inv_freq) features are rotated."""
     dev = _device(q, "q")
     T, Hq, D = q.shape
-    _need((k is None) == (v is None) and (k is None) == (k_cache is None) and (k is None) == (v_cache is None),
-          "q4_rope_append_run: k, v and the caches come together")
+    dtype, t16 = q.dtype, q_out.dtype
+    f32, i32 = _Types.f32, _Types.i32
+    d = Q4_F32 if dtype is f32 else _dtype(q)
+    qa, qs = _heads(dev, q, "q", T, Hq, D, dtype)
     if k is not None:
+        _need(v is not None and k_cache is not None and v_cache is not None,
+              "q4_rope_append_run: k, v and the caches come together")
         cache = _cache(dev, k_cache, v_cache)
-        _need(cache.D == D and k.shape[1] == cache.heads and v.shape == k.shape and
-              q_out.dtype is k_cache.dtype, "q4_rope_append_run: shapes or types do not agree")
+        _need(cache[4] == D and t16 is k_cache.dtype, "q4_rope_append_run: shapes or types do not agree")
+        ka, ks = _heads(dev, k, "k", T, cache[3], D, dtype)
+        va, vs = _heads(dev, v, "v", T, cache[3], D, dtype)
     else:
-        cache = _KvCache(None, None, _half_dtype(q_out, "q_out"), 1, D, 1, 0, 0, 0, 0)
-    _need(q_out.shape == q.shape and (positions is None or positions.numel() == T) and
+        _need(v is None and k_cache is None and v_cache is None, "q4_rope_append_run: k, v and the caches come together")
+        cache = (0, 0, _half_dtype(q_out, "q_out"), 1, D, 1, 0, 0, 0, 0)
+        ka = va = ks = vs = 0
+    _need(q_out.shape == (T, Hq, D) and (positions is None or positions.numel() == T) and
           (slots is None or slots.numel() == T) and (q_gamma is None or q_gamma.numel() == D) and
           (k_gamma is None or k_gamma.numel() == D), "q4_rope_append_run: shapes do not agree")
-    d = _dtype(q)
-    qa, qs = _heads(dev, q, "q", T, D, q.dtype)
-    ka, ks = _heads(dev, k, "k", T, D, q.dtype) if k is not None else (None, 0)
-    va, vs = _heads(dev, v, "v", T, D, q.dtype) if k is not None else (None, 0)
-    a = _RopeAppend(T, Hq, d, 2 * inv_freq.numel() if inv_freq is not None else 0, layout, scale, eps, qa, ka, va,
-                    qs, ks, vs, _on(dev, q_gamma, "q_gamma", _Types.f32), _on(dev, k_gamma, "k_gamma", _Types.f32),
-                    _on(dev, positions, "positions", _Types.i32), _on(dev, inv_freq, "inv_freq", _Types.f32),
-                    _on(dev, slots, "slots", _Types.i32), _on(dev, q_out, "q_out", q_out.dtype), cache)
-    st = lib().q4_rope_append_run(ctypes.byref(a), _options(flags, None), _stream(stream))
+    a = _ROPE.pack(T, Hq, d, 2 * inv_freq.numel() if inv_freq is not None else 0, layout, scale, eps, qa, ka, va, qs, ks,
+                   vs, _on(dev, q_gamma, "q_gamma", f32), _on(dev, k_gamma, "k_gamma", f32),
+                   _on(dev, positions, "positions", i32), _on(dev, inv_freq, "inv_freq", f32),
+                   _on(dev, slots, "slots", i32), _on(dev, q_out, "q_out", t16), *cache)
+    st = lib().q4_rope_append_run(a, _options(flags, None), _stream(stream))
     if check:
         _check(st, "q4_rope_append_run")
     return st
@@ -824,26 +842,30 @@ def q4_prefix_attn_run(q, k_cache, v_cache, out, workspace, group_offsets=None, 
     own_pages [S, pages]).  scale None: 1 / sqrt(D).  out [S, Hq, D], lse [S, Hq] float32."""
     dev = _device(q, "q")
     S, Hq, D = q.shape
+    t16, i32 = k_cache.dtype, _Types.i32
     cache = _cache(dev, k_cache, v_cache)
-    groups = shared_lens.numel() if shared_lens is not None else 0
-    _need((shared_lens is None) == (shared_pages is None) and (own_lens is None) == (own_pages is None) and
-          cache.D == D and out.shape == q.shape and
-          (groups == 0 or (shared_pages.dim() == 2 and shared_pages.shape[0] == groups and
-                           (group_offsets is None or group_offsets.numel() == groups + 1))) and
-          (own_lens is None or (own_pages.dim() == 2 and own_pages.shape[0] == S and own_lens.numel() == S)) and
-          (limits is None or limits.numel() == S) and (lse is None or lse.shape == (S, Hq)),
-          "q4_prefix_attn_run: shapes do not agree")
-    qa, qs = _heads(dev, q, "q", S, D, k_cache.dtype)
-    i32 = _Types.i32
-    out_dtype = Q4_F32 if out.dtype is _Types.f32 else _half_dtype(out, "out")
-    a = _PrefixAttn(S, Hq, groups, out_dtype, shared_pages.shape[1] if groups else 0,
-                    own_pages.shape[1] if own_pages is not None else 0, D ** -0.5 if scale is None else scale, qa, qs,
-                    cache, _on(dev, group_offsets, "group_offsets", i32), _on(dev, shared_pages, "shared_pages", i32),
-                    _on(dev, shared_lens, "shared_lens", i32), _on(dev, limits, "limits", i32),
-                    _on(dev, own_pages, "own_pages", i32), _on(dev, own_lens, "own_lens", i32),
-                    _on(dev, out, "out", out.dtype), _on(dev, lse, "lse", _Types.f32),
-                    _on(dev, workspace, "workspace", _Types.u8), workspace.numel())
-    st = lib().q4_prefix_attn_run(ctypes.byref(a), _options(flags, wait_timeout_ns), _stream(stream))
+    groups = most_shared = most_own = 0
+    if shared_lens is not None or shared_pages is not None:
+        _need(shared_lens is not None and shared_pages is not None, "q4_prefix_attn_run: shared_lens and shared_pages come together")
+        groups = shared_lens.numel()
+        rows, most_shared = shared_pages.shape
+        _need(rows == groups and (group_offsets is None or group_offsets.numel() == groups + 1),
+              "q4_prefix_attn_run: shapes do not agree")
+    if own_lens is not None or own_pages is not None:
+        _need(own_lens is not None and own_pages is not None, "q4_prefix_attn_run: own_lens and own_pages come together")
+        rows, most_own = own_pages.shape
+        _need(rows == S and own_lens.numel() == S, "q4_prefix_attn_run: shapes do not agree")
+    _need(cache[4] == D and out.shape == (S, Hq, D) and (limits is None or limits.numel() == S) and
+          (lse is None or lse.shape == (S, Hq)), "q4_prefix_attn_run: shapes do not agree")
+    qa, qs = _heads(dev, q, "q", S, Hq, D, t16)
+    o = out.dtype
+    out_dtype = cache[2] if o is t16 else Q4_F32 if o is _Types.f32 else _half_dtype(out, "out")
+    a = _ATTN.pack(S, Hq, groups, out_dtype, most_shared, most_own, D ** -0.5 if scale is None else scale, qa, qs, *cache,
+                   _on(dev, group_offsets, "group_offsets", i32), _on(dev, shared_pages, "shared_pages", i32),
+                   _on(dev, shared_lens, "shared_lens", i32), _on(dev, limits, "limits", i32),
+                   _on(dev, own_pages, "own_pages", i32), _on(dev, own_lens, "own_lens", i32), _on(dev, out, "out", o),
+                   _on(dev, lse, "lse", _Types.f32), _on(dev, workspace, "workspace", _Types.u8), workspace.numel())
+    st = lib().q4_prefix_attn_run(a, _options(flags, wait_timeout_ns), _stream(stream))
     if check:
         _check(st, "q4_prefix_attn_run")
     return st
@@ -864,8 +886,7 @@ def q4_beam_step_run(logits, scores, tokens, parents, out_scores, workspace, fin
     groups, W = scores.shape
     of = tokens.shape
     stride = logits.stride()
-    _need(rows == groups * W and len(of) == 2 and of[0] == groups and parents.shape == of and
-          out_scores.shape == of and (finished is None or finished.shape == scores.shape) and
+    _need(rows == groups * W and len(of) == 2 and of[0] == groups and parents.shape == of and out_scores.shape == of and (finished is None or finished.shape == scores.shape) and
           (out_finished is None or out_finished.shape == of) and logits.dtype is _Types.f32 and stride[1] == 1,
           "q4_beam_step_run: shapes or types do not agree")
     i32, f32, u8 = _Types.i32, _Types.f32, _Types.u8
@@ -893,11 +914,11 @@ def q4_beam_reorder_run(tables, lens, parents, spare, out_tables, out_spare, poo
     _need(n == groups * W and lens.numel() == groups and spare.numel() == n and out_spare.numel() == n and
           out_tables.shape == tables.shape and stride[4] == 1, "q4_beam_reorder_run: shapes do not agree")
     i32, e = _Types.i32, pool.element_size()
-    a = _BeamReorder(groups, W, most, planes, heads, page, pages, D * e, stride[0] * e, stride[1] * e, stride[2] * e,
-                     stride[3] * e, pool.data_ptr(), _on(dev, tables, "tables", i32), _on(dev, lens, "lens", i32),
-                     _on(dev, parents, "parents", i32), _on(dev, spare, "spare", i32),
-                     _on(dev, out_tables, "out_tables", i32), _on(dev, out_spare, "out_spare", i32))
-    st = lib().q4_beam_reorder_run(ctypes.byref(a), _options(flags, None), _stream(stream))
+    a = _REORDER.pack(groups, W, most, planes, heads, page, pages, D * e, stride[0] * e, stride[1] * e, stride[2] * e,
+                      stride[3] * e, pool.data_ptr(), _on(dev, tables, "tables", i32), _on(dev, lens, "lens", i32),
+                      _on(dev, parents, "parents", i32), _on(dev, spare, "spare", i32),
+                      _on(dev, out_tables, "out_tables", i32), _on(dev, out_spare, "out_spare", i32))
+    st = lib().q4_beam_reorder_run(a, _options(flags, None), _stream(stream))
     if check:
         _check(st, "q4_beam_reorder_run")
     return st

@@ -202,6 +202,19 @@ def test_struct_layouts_match_the_header(tmp_path):
         assert line.split() == [name] + [str(v) for v in want]
 
 
+def test_packed_structures_match_the_layouts():
+    """The binding packs the structures as bytes: sizes and places of the fields."""
+    for packer, s in ((q4._ROPE, q4._RopeAppend), (q4._ATTN, q4._PrefixAttn), (q4._REORDER, q4._BeamReorder)):
+        assert packer.size == ctypes.sizeof(s)
+        flat = []
+        for name, kind in s._fields_:
+            flat += [(name, f) for f, _ in kind._fields_] if hasattr(kind, "_fields_") else [(name, None)]
+        a = s.from_buffer_copy(packer.pack(*range(1, len(flat) + 1)))
+        for i, (name, inner) in enumerate(flat):
+            have = getattr(a, name) if inner is None else getattr(getattr(a, name), inner)
+            assert have == i + 1, (name, inner)
+
+
 def test_binding_refuses_tensors_that_are_not_on_a_gpu():
     import torch
     x = torch.zeros(2, 4, 64)
