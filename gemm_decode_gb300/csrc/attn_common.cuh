@@ -30,7 +30,7 @@ namespace q4 {
 using namespace tc;
 
 constexpr int kManyKeys = 128, kFewKeys = 64;   // keys of a unit
-constexpr int kManyCost = 1, kFewCost = 1;      // units that a segment's beginning and end count for
+constexpr int kManyCost = 2, kFewCost = 2;      // units that a segment's beginning and end count for
 constexpr int kFewRows = 16;                    // rows of a segment of the kernel for few rows
 constexpr int kManyTiles = 2;                   // tiles of 128 rows of one segment of the kernel for many
 

@@ -93,6 +93,17 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
     asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// 32 bytes of a row, a sector in one go where it is aligned (each lane has a row of its own).
+__device__ __forceinline__ void put32(void *to, const uint32_t *w, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const float *f) {
     tmem_st16(addr, reinterpret_cast<const uint32_t *>(f));
@@ -462,6 +473,7 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const int64_t part = s.whole ? at : static_cast<int64_t>(s.slot) * (128 * kManyTiles) + t * 128 + row;
             const bool write = have && ib(query >= 0 && query < g.S && head < g.Hq && s.slot < 2 * g.many_ctas);
             const float f = final ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+            const bool wide = !final || reinterpret_cast<uintptr_t>(g.out) % 32 == 0;   // (rows are multiples of 32 bytes)
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float v[32];
@@ -475,20 +487,21 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
                 if (write) {
                     if (final && !g.out_f32) {
-                        uint4 *to = reinterpret_cast<uint4 *>(static_cast<C *>(g.out) + at * D + c);
+                        uint32_t w[16];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            to[i] = make_uint4(pack2<C>(v[8 * i] * f, v[8 * i + 1] * f),
-                                               pack2<C>(v[8 * i + 2] * f, v[8 * i + 3] * f),
-                                               pack2<C>(v[8 * i + 4] * f, v[8 * i + 5] * f),
-                                               pack2<C>(v[8 * i + 6] * f, v[8 * i + 7] * f));
+                        for (int i = 0; i < 16; ++i) w[i] = pack2<C>(v[2 * i] * f, v[2 * i + 1] * f);
+                        put32(static_cast<C *>(g.out) + at * D + c, w, wide);
+                        put32(static_cast<C *>(g.out) + at * D + c + 16, w + 8, wide);
                     } else {
-                        float *base = final ? static_cast<float *>(g.out) + at * D
-                                            : (s.whole ? g.whole[0] : g.many_part) + part * D;
+                        float *to = (final ? static_cast<float *>(g.out) + at * D
+                                           : (s.whole ? g.whole[0] : g.many_part) + part * D) + c;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            reinterpret_cast<float4 *>(base + c)[i] =
-                                make_float4(v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f);
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[i + k] * f);
+                            put32(to + i, w, wide);
+                        }
                     }
                 }
                 __syncwarp();
