@@ -11,7 +11,11 @@
 // One warp brings units of 64 keys into a ring of stages (bulk tensor copies, a box per page or
 // 64 rows of one, 128-byte swizzle), four warps compute: each takes 16 of a unit's keys, with a
 // running maximum, sum and accumulators of its own, joined in a fixed order when the segment
-// ends.
+// ends.  Two CTAs to an SM, three stages of 32 KB each (128 features).
+//
+// Measured (cold caches): own segments of 64 sequences, 768 keys on average, 8 heads of 128
+// (201 MB) 38 us, 5.3 TB/s, 0.78 of measured; of 256 sequences, 218 keys (228 MB) 49 us: there a
+// segment is four units, and its queries' loads and its join cost two.
 #pragma once
 
 #include "attn_common.cuh"

@@ -8,6 +8,10 @@
 //            the call allow none)
 //   few      the others (likewise)
 //   join     adds the parts of each row, where several kernels or CTAs have one
+//
+// The four are launched overlapped.  Four beams of a prompt of 1000 tokens take 15 us, most of
+// it latency: the plan 3-4 us (13 us for a prompt of 4096 queries with a limit each before its
+// tables lay in shared memory and its records were those that are read), the join 5.
 #include <algorithm>
 #include <atomic>
 
@@ -111,7 +115,33 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
     };
     // ---- groups: offsets in order, and the first run of each
     int carry_off = 0, all_runs = 0;
-    if (g.groups > 0) {
+    bool any_few = own || g.groups >= 32;   // whether there can be entries of few rows
+    if (g.groups > 0 && g.groups < 32) {   // each warp for itself, a place a lane
+        const int i = t & 31;
+        int off = 0, len = 0;
+        if (i <= g.groups) off = g.group_offsets != nullptr ? min(max(g.group_offsets[i], 0), g.S) : (i == 0 ? 0 : g.S);
+        if (i < g.groups) len = clamp_len(g.shared_lens[i], g.max_shared, g.page);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(~0u, off, o);
+            if (i >= o) off = max(off, n);
+        }
+        const int n = off - __shfl_up_sync(~0u, off, 1);
+        int runs = i > 0 && i <= g.groups && !few_group(n) ? (n + run - 1) / run : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int r = __shfl_up_sync(~0u, runs, o);
+            if (i >= o) runs += r;
+        }
+        all_runs = __shfl_sync(~0u, runs, g.groups);
+        any_few |= __any_sync(~0u, i > 0 && i <= g.groups && n > 0 && few_group(n)) != 0;
+        if (t <= g.groups) {
+            s_first[t] = off;
+            s_run[t] = runs;
+            if (t < g.groups) s_len[t] = len;
+        }
+        __syncthreads();
+    } else if (g.groups > 0) {
         for (int g0 = 0; g0 <= g.groups; g0 += T) {
             const int i = g0 + t;
             int off = 0;
@@ -160,7 +190,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
                         keys = max(0, min(group_len(group), seen[i]));
                     }
                 }
-                if (__match_any_sync(~0u, r) == ~0u) {
+                if (__reduce_min_sync(~0u, r) == __reduce_max_sync(~0u, r)) {
                     keys = __reduce_max_sync(~0u, keys);
                     if (r >= 0 && (t & 31) == 0) atomicMax(run_keys + r, keys);
                 } else if (r >= 0) {
@@ -198,7 +228,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
     }
     if (t == 0) *g.many = AttnCounts{units0, entries0, 0};
     // ---- entries of few rows: own segments, then small groups
-    const int places = (own ? g.S : 0) + g.groups;
+    const int places = any_few ? (own ? g.S : 0) + g.groups : 0;
     int64_t units1 = 0;
     int entries1 = 0;
     for (int p0 = 0; p0 < places; p0 += T) {
@@ -228,24 +258,34 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
             g.few_start[entries1 + e - 1] = start;
         }
         if (own && p < g.S) g.places[g.S + p] = AttnPlace{start, units, 0, 0, tiles, {}};
-        if (a.group >= 0)   // a small group's queries, 16 at most
+        if (a.group >= 0)   // a small group's queries, 16 at most (with no key among them: 0 units)
             for (int i = 0; i < a.queries; ++i) g.places[a.first + i] = AttnPlace{start, units, 0, i, tiles, {}};
         units1 += tu;
         entries1 += te;
     }
     if (t == 0) *g.few = AttnCounts{units1, entries1, 0};
-    // ---- the other queries' places (runs: written above, by other threads)
+    // ---- the other queries' places (runs: written above, by other threads).  A call with shared
+    // segments alone looks at nothing of them but whether there is a key.
     if (g.groups > 0) {
         __syncthreads();
+        int group = 0;   // of the query before, as a rule
         for (int s = t; s < g.S; s += T) {
             AttnPlace at = {};
             if (s >= first_of[0] && s < first_of[g.groups]) {
-                const int group = last_at_most(first_of, g.groups, s), first = first_of[group];
+                if (s < first_of[group] || s >= first_of[group + 1]) group = last_at_most(first_of, g.groups, s);
+                const int first = first_of[group];
                 if (few_group(first_of[group + 1] - first)) continue;
                 const int r = (s - first) / run, keys = run_keys[run_of[group] + r];
-                at = AttnPlace{run_start[run_of[group] + r], (keys + kManyKeys - 1) / kManyKeys, 1, (s - first) - r * run, 1, {}};
+                at.units = (keys + kManyKeys - 1) / kManyKeys;
+                if (own) {
+                    at.start = run_start[run_of[group] + r];
+                    at.many = 1;
+                    at.place = (s - first) - r * run;
+                    at.tiles = 1;
+                }
             }
-            g.places[s] = at;
+            if (own) g.places[s] = at;
+            else g.places[s].units = at.units;
         }
     }
 }
