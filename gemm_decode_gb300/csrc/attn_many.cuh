@@ -4,7 +4,7 @@
 // 128) by the keys, in tiles of 128 keys:
 //   S = Q K^T      operands in shared memory (128-byte swizzle), sums in tensor memory
 //   P = exp2(scale2 S - m)   a thread has a row: 128 scores from tensor memory to registers,
-//                  their maximum, the weights rounded to 16 bits back over the scores' columns
+//                  their maximum, then the weights, rounded to 16 bits back over the scores' columns
 //   O += P V       operand A in tensor memory, the values as they lie (their features side by
 //                  side: the operand is read transposed)
 // The maximum that a row's weights are relative to is renewed only when it has grown by more
@@ -17,6 +17,18 @@
 //   warp 1      the MMAs: the warp walks the loop, one elected lane issues.  The scores of one
 //               tile of rows are formed while the weights of the other are computed.
 //   warps 4-7, 8-11  weights of the first and second tile of rows, and the results
+// (warps 2 and 3 do nothing: registers are handed from the first four warps to the others by
+// groups of four)
+//
+// What bounds it: a unit (256 rows by 128 keys of 128 features) takes 3100 cycles, of which the
+// tensor core needs 2048 at its rate.  Without any waiting for weights its products take 2540:
+// the operands of S, both in shared memory, are read at the 128 bytes a cycle that it gives, and
+// the copies of keys and values write there too.  The other 560 are the hand-overs between the
+// MMAs and the weights (weights without exponentials: 3050).  A segment's beginning and end cost
+// about 2.4 units: the first scores and weights, and the results out of tensor memory.
+// Measured (graphs): 256 queries x 32 heads by 27900 keys of 8 heads 97 us, 1.2 PFLOP/s (0.63 of
+// measured bf16); a causal prompt of 4096 tokens 150 us with plan and join, 0.9 PFLOP/s.
+// Results stored 16 bytes a lane instead of whole sectors: 26 us more for the prompt.
 #pragma once
 
 #include "attn_common.cuh"
@@ -86,11 +98,6 @@ __device__ __forceinline__ void pin32(float *f) {
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-__device__ __forceinline__ float min3(float a, float b, float c) {
-    float r;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 // 32 bytes of a row, a sector in one go where it is aligned (each lane has a row of its own).
@@ -255,7 +262,8 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         Ring<M::kStages> r;
         uint32_t q_ph = 0, p_ph[2] = {0, 0}, oe_ph[2] = {0, 0};
         const uint32_t bf16 = std::is_same<C, __nv_bfloat16>::value;
-        const uint32_t idesc_s = idesc_f16(bf16 != 0, 128, kManyKeys);
+        // a scale below zero: the products of the queries' negatives (bit 13)
+        const uint32_t idesc_s = idesc_f16(bf16 != 0, 128, kManyKeys) | (g.scale2 < 0.0f ? 1u << 13 : 0u);
         const uint32_t idesc_o = idesc_f16(bf16 != 0, 128, D) | (1u << 16);   // operand B read transposed
         const uint64_t q_desc = umma_desc(smem_addr(q_tiles)), k_desc = umma_desc(smem_addr(ring));
         const uint64_t v_desc = umma_desc_mn(smem_addr(ring), M::kHalfBytes);
@@ -360,7 +368,7 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const int row = (warp & 3) * 32 + lane;               // lane of tensor memory
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + s_cols + t * kManyKeys, o_at = tmem + lanes + o_cols + t * D;
-        const float off = g.scale2 >= 0.0f ? neg_inf() : -neg_inf();
+        const float scale2 = fabsf(g.scale2);   // (a sign below zero is in the scores already)
         uint32_t s_ph = 0, o_ph = 0;
         bool ok = true;
         while (ok && next()) {
@@ -389,45 +397,15 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 if (!__all_sync(~0u, seen >= kManyKeys || !have)) {
 #pragma unroll
                     for (int c = 0; c < kManyKeys; ++c)
-                        if (c >= seen) x[c] = off;
+                        if (c >= seen) x[c] = neg_inf();
                 }
-                // The weights of the first keys, relative to the maximum so far, and meanwhile the
-                // largest score (the smallest, times a scale below zero): only where that has
-                // outgrown the maximum, the weights are formed again.
-                uint32_t p[kManyKeys / 2];
-                float2 sum[2];
-                auto weigh = [&](int from, int until) {
-                    const float b = m == neg_inf() ? 0.0f : -m;
-                    const float2 base = make_float2(b, b), scale = make_float2(g.scale2, g.scale2);
+                float top = max3(x[0], x[1], x[2]), top1 = max3(x[3], x[4], x[5]);
 #pragma unroll
-                    for (int i = from; i < until; i += 2) {
-                        const float2 y = __ffma2_rn(make_float2(x[i], x[i + 1]), scale, base);
-                        const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-                        sum[(i / 2) % 2] = __fadd2_rn(sum[(i / 2) % 2], e);
-                        p[i / 2] = pack2<C>(e.x, e.y);
-                    }
-                };
-                sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-                weigh(0, kFirstKeys);
-                float top;
-                if (g.scale2 >= 0.0f) {
-                    float a = max3(x[0], x[1], x[2]), b = max3(x[3], x[4], x[5]);
-#pragma unroll
-                    for (int c = 6; c + 3 < kManyKeys; c += 4) {
-                        a = max3(a, x[c], x[c + 1]);
-                        b = max3(b, x[c + 2], x[c + 3]);
-                    }
-                    top = max3(a, b, fmaxf(x[kManyKeys - 2], x[kManyKeys - 1]));
-                } else {
-                    float a = min3(x[0], x[1], x[2]), b = min3(x[3], x[4], x[5]);
-#pragma unroll
-                    for (int c = 6; c + 3 < kManyKeys; c += 4) {
-                        a = min3(a, x[c], x[c + 1]);
-                        b = min3(b, x[c + 2], x[c + 3]);
-                    }
-                    top = min3(a, b, fminf(x[kManyKeys - 2], x[kManyKeys - 1]));
+                for (int c = 6; c + 3 < kManyKeys; c += 4) {
+                    top = max3(top, x[c], x[c + 1]);
+                    top1 = max3(top1, x[c + 2], x[c + 3]);
                 }
-                top *= g.scale2;
+                top = scale2 * max3(top, top1, fmaxf(x[kManyKeys - 2], x[kManyKeys - 1]));
                 const bool renew = have && (top > m + 8.0f || (m == neg_inf() && top > m));
                 if (__any_sync(~0u, renew)) {
                     float f = 1.0f;
@@ -448,12 +426,25 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             tmem_st32(o_at + c, v);
                         }
                     }
-                    sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-                    weigh(0, kFirstKeys);
                 }
+                // (the code of a tile's weights stands here once: fetching it is what a short call waits for)
+                uint32_t p[kManyKeys / 2];
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                const float b = m == neg_inf() ? 0.0f : -m;
+                const float2 base = make_float2(b, b), scale = make_float2(scale2, scale2);
+                auto weigh = [&](int from, int until) {
+#pragma unroll
+                    for (int i = from; i < until; i += 2) {
+                        const float2 y = __ffma2_rn(make_float2(x[i], x[i + 1]), scale, base);
+                        const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                        sum[(i / 2) % 2] = __fadd2_rn(sum[(i / 2) % 2], e);
+                        p[i / 2] = pack2<C>(e.x, e.y);
+                    }
+                };
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
-                    if (part == 1) weigh(kFirstKeys, kManyKeys);
+                    if (part == 0) weigh(0, kFirstKeys);
+                    else weigh(kFirstKeys, kManyKeys);
 #pragma unroll
                     for (int c = part == 0 ? 0 : kFirstKeys; c < (part == 0 ? kFirstKeys : kManyKeys); c += 32)
                         tmem_st16(s_at + c / 2, p + c / 2);
@@ -474,38 +465,38 @@ attn_many_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const bool write = have && ib(query >= 0 && query < g.S && head < g.Hq && s.slot < 2 * g.many_ctas);
             const float f = final ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
             const bool wide = !final || reinterpret_cast<uintptr_t>(g.out) % 32 == 0;   // (rows are multiples of 32 bytes)
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float v[32];
-                tmem_ld32(o_at + c, v);
-                tmem_ld_wait();
-                pin32(v);
-                if (c + 32 == D) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(o_empty(t));
-                }
-                if (write) {
-                    if (final && !g.out_f32) {
-                        uint32_t w[16];
+            // all of the row at once, so that the next segment's products may begin
+            float v[D];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = pack2<C>(v[2 * i] * f, v[2 * i + 1] * f);
-                        put32(static_cast<C *>(g.out) + at * D + c, w, wide);
-                        put32(static_cast<C *>(g.out) + at * D + c + 16, w + 8, wide);
-                    } else {
-                        float *to = (final ? static_cast<float *>(g.out) + at * D
-                                           : (s.whole ? g.whole[0] : g.many_part) + part * D) + c;
+            for (int c = 0; c < D; c += 32) tmem_ld32(o_at + c, v + c);
+            tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint32_t w[8];
+            for (int c = 0; c < D; c += 32) pin32(v + c);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_empty(t));
+            if (write) {
+                if (final && !g.out_f32) {
+                    C *to = static_cast<C *>(g.out) + at * D;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[i + k] * f);
-                            put32(to + i, w, wide);
-                        }
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = pack2<C>(v[c + 2 * i] * f, v[c + 2 * i + 1] * f);
+                        put32(to + c, w, wide);
+                    }
+                } else {
+                    float *to = final ? static_cast<float *>(g.out) + at * D : (s.whole ? g.whole[0] : g.many_part) + part * D;
+#pragma unroll
+                    for (int c = 0; c < D; c += 8) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[c + i] * f);
+                        put32(to + c, w, wide);
                     }
                 }
-                __syncwarp();
             }
+            __syncwarp();
             if (write) {
                 if (!final) (s.whole ? g.whole_stats[0] : g.many_stats)[part] = make_float2(m, l);
                 else if (g.lse != nullptr) g.lse[at] = lse_of(m, l);
