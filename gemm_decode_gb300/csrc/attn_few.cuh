@@ -284,6 +284,11 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
                     mma16816<C>(o[n + 1], p, b[2], b[3]);
                 }
             }
+            // The stage goes back to copies, which write it through the asynchronous proxy: every
+            // lane's reads are ordered before them.  An arrival alone lets a copy overtake matrix
+            // loads whose products come later (without the fence, 20 to 570 of 2048 segments had
+            // the last chunks of their values from another unit, at random).
+            fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(empty(r.s));
             r.step();

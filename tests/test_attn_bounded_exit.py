@@ -55,3 +55,11 @@ def test_the_registers_of_the_roles_fit_the_launch():
     dec, inc = (int(re.search(r"setmaxnreg\.%s\.sync\.aligned\.u32 (\d+)" % w, text).group(1)) for w in ("dec", "inc"))
     launched = 65536 // threads // 8 * 8   # registers a thread at the launch, one block an SM
     assert 128 * dec + (threads - 128) * inc <= threads * launched
+
+
+def test_a_stage_is_given_back_behind_a_fence():
+    """Copies write a stage through another proxy than the matrix loads that read it."""
+    text = source("attn_few.cuh")
+    back = [m.start() for m in re.finditer(r"mbar_arrive\(empty\(", text)]
+    assert len(back) == 1
+    assert re.search(r"\n {12}fence_proxy_async\(\);\n {12}__syncwarp\(\);\n {12}if \(lane == 0\) $", text[:back[0]])

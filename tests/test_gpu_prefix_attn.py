@@ -304,3 +304,19 @@ def test_a_prompt_and_a_search_in_one_workspace(torch):
     ws = torch.full((q4.q4_prefix_attn_workspace(300, 2, 8, 2, 128),), 255, device="cuda", dtype=torch.uint8)
     for p in (a, b, c, a, c, b):
         check(torch, p, ws=ws, flags=q4.Q4_RUN_OVERLAPPED)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_large_batch_is_the_same_every_time(torch, D):
+    """Every SM with several segments of both kinds, over and over with no wait between the calls:
+    what a register, a stage or a part holds too early or too late shows as another result."""
+    S = 192
+    own = [(37 * i) % 300 for i in range(S)]
+    p = problem(torch, [S], [5000], own, 32, 8, D, 64, torch.bfloat16, stale=False)
+    ws = torch.empty(q4.q4_prefix_attn_workspace(S, 1, 32, 8, D), device="cuda", dtype=torch.uint8)
+    first, lse = run(torch, p, ws=ws)
+    again = [run(torch, p, ws=ws) for _ in range(40)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, a) and torch.equal(lse, b) for a, b in again)
+    check(torch, {n: (v[:8] if n in ("q", "own_pages", "own_lens") else v) for n, v in p.items()} |
+          {"group_offsets": torch.tensor([0, 8], device="cuda", dtype=torch.int32)})
