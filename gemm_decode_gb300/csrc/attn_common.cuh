@@ -79,6 +79,7 @@ struct AttnArgs {
     int *run_keys;       // [runs] the most keys that a query of the run sees
     int64_t *run_start;  // [runs] first unit of the run
     int many_ctas, few_ctas;
+    int beside_many;             // the kernel for few rows runs beside the one for many
     float *many_part, *few_part;     // [2 CTAs][rows][D]
     float2 *many_stats, *few_stats;  // [2 CTAs][rows]: maximum, sum of weights
     float *whole[2];                 // [S][Hq][D]: shared, own
@@ -101,8 +102,21 @@ __device__ __forceinline__ int clamp_len(int n, int most_pages, int page) {
 
 // CTAs that take part (each has a unit), the units that CTA c of them takes, and the CTA that
 // takes unit u.
-__device__ __forceinline__ int ctas_of(int64_t units, int most) {
-    return units < most ? static_cast<int>(units) : most;
+__device__ __forceinline__ int few_ctas_of(const AttnArgs &g, int64_t few) {
+    return few < g.few_ctas ? static_cast<int>(few) : g.few_ctas;
+}
+// The two kernels run at the same time, on different SMs.  Where the few rows have far more to do
+// (eight times the units), the many rows take no more CTAs than have five units each, and the
+// other SMs read keys and values meanwhile.  64 sequences behind one prefix (18 times): 75 us
+// with a unit each, 69 with five, 72 with eight, 80 with twelve; 16 prompts of 8 beams (twice)
+// 29.5 with one, 30.7 with five.
+__device__ __forceinline__ int many_ctas_of(const AttnArgs &g, int64_t many, int64_t few) {
+    const int64_t n = few >= 8 * many ? (many + 4) / 5 : many;
+    return n < g.many_ctas ? static_cast<int>(n) : g.many_ctas;
+}
+__device__ __forceinline__ AttnCounts counts_at(const AttnCounts *n) {
+    const int4 raw = __ldcg(reinterpret_cast<const int4 *>(n));
+    return AttnCounts{static_cast<int64_t>(static_cast<uint32_t>(raw.x)) | static_cast<int64_t>(raw.y) << 32, raw.z, 0};
 }
 // (divisions in 32 bits where the numbers allow it: in 64 they take several hundred cycles)
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -151,19 +165,17 @@ struct AttnWalk {
     const int64_t *start;
 
     // To the CTA's first unit, by a warp.
-    __device__ __forceinline__ void begin(const AttnCounts *n, const AttnEntry *all, const int64_t *starts, int most,
+    __device__ __forceinline__ void begin(const AttnCounts &n, const AttnEntry *all, const int64_t *starts, int ctas,
                                           int lane) {
-        const int4 raw = __ldcg(reinterpret_cast<const int4 *>(n));
-        const int64_t units = static_cast<int64_t>(static_cast<uint32_t>(raw.x)) | static_cast<int64_t>(raw.y) << 32;
-        const int ctas = ctas_of(units, most);
+        const int64_t units = n.units;
         const bool takes_part = static_cast<int>(blockIdx.x) < ctas;
         entries = all;
         start = starts;
         at = takes_part ? units_before(units, ctas, blockIdx.x) : 0;
         end = takes_part ? units_before(units, ctas, blockIdx.x + 1) : 0;
-        const int lo = at < end ? entry_at(start, raw.z, at, lane) : 0;
+        const int lo = at < end ? entry_at(start, n.entries, at, lane) : 0;
         entry = first = lo;
-        left_ = raw.z - lo;
+        left_ = n.entries - lo;
     }
     // The entries from the first on into shared memory, by all threads (a barrier is to follow).
     __device__ __forceinline__ void hold(AttnHeld *to) {
@@ -211,7 +223,7 @@ __device__ __forceinline__ void row_of(const AttnArgs &g, const AttnSegment &s, 
 // Keys of the segment that a query sees.
 __device__ __forceinline__ int limit_of(const AttnArgs &g, const AttnSegment &s, int query) {
     if (s.e.group < 0 || g.limits == nullptr) return s.e.keys;
-    return max(0, min(s.e.keys, g.limits[query]));
+    return max(0, min(s.e.keys, __ldcg(g.limits + query)));
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z,

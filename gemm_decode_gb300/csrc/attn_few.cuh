@@ -92,7 +92,11 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    wait_prior_grid();
+    // Beside the kernel for many rows, which is the one before: it lets this one start only after
+    // it has waited for the plan itself, and nothing that is read here comes from it, so it is
+    // waited for at the end (the kernel behind reads the results of both).  What the plan and the
+    // kernels before it wrote is read past the first-level cache.
+    if (!g.beside_many) wait_prior_grid();
     allow_next_grid();
 
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -110,7 +114,10 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
     };
 
     AttnWalk<kFewKeys, kFewCost, true> walk;
-    walk.begin(g.few, g.few_entries, g.few_start, g.few_ctas, lane);
+    {
+        const AttnCounts few = counts_at(g.few);
+        walk.begin(few, g.few_entries, g.few_start, few_ctas_of(g, few.units), lane);
+    }
     walk.hold(held);
     __syncthreads();
     AttnSegment s;
@@ -133,7 +140,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
                 int id = g.pages;
                 if (lane < copies && key < s.e.keys &&
                     ib((key >> g.page_shift) < (s.e.group < 0 ? g.max_own : g.max_shared)))
-                    id = table[key >> g.page_shift];
+                    id = __ldcg(table + (key >> g.page_shift));
                 return id < 0 || id > g.pages ? g.pages : id;
             };
             int page = page_of(s.u0);
@@ -156,6 +163,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
         for (int64_t j = issued > F::kStages ? issued - F::kStages : 0; j < issued; ++j)
             mbar_wait(full(static_cast<int>(j % F::kStages)), static_cast<uint32_t>(j / F::kStages) & 1u,
                       50ull * 1000 * 1000);
+        if (g.beside_many) wait_prior_grid();
         return;
     }
 
@@ -193,8 +201,8 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
             const C *src = static_cast<const C *>(g.q) + query * g.q_stride + static_cast<int64_t>(head) * D + col0;
 #pragma unroll
             for (int k = 0; k < kK; ++k) {
-                q[k][i] = have ? *reinterpret_cast<const uint32_t *>(src + 16 * k) : 0u;
-                q[k][i + 2] = have ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8) : 0u;
+                q[k][i] = have ? __ldcg(reinterpret_cast<const uint32_t *>(src + 16 * k)) : 0u;
+                q[k][i + 2] = have ? __ldcg(reinterpret_cast<const uint32_t *>(src + 16 * k + 8)) : 0u;
             }
         }
         float o[kN][4];
@@ -372,6 +380,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
             }
         }
     }
+    if (g.beside_many) wait_prior_grid();
 }
 
 }  // namespace q4

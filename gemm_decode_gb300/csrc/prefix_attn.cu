@@ -9,9 +9,11 @@
 //   few      the others (likewise)
 //   join     adds the parts of each row, where several kernels or CTAs have one
 //
-// The four are launched overlapped.  Four beams of a prompt of 1000 tokens take 15 us, most of
-// it latency: the plan 3-4 us (13 us for a prompt of 4096 queries with a limit each before its
-// tables lay in shared memory and its records were those that are read), the join 5.
+// The four are launched overlapped, and the kernels for many and few rows run side by side (256
+// sequences: 162 us one after the other, 158 so).  Four beams of a prompt of 1000 tokens take
+// 16 us, most of it latency: the plan 3-4 us (13 us for a prompt of 4096 queries with a limit
+// each before its tables lay in shared memory and its records were those that are read), the
+// join 5.
 #include <algorithm>
 #include <atomic>
 
@@ -310,12 +312,13 @@ struct AttnParts {
     }
 };
 
-__device__ __forceinline__ AttnParts parts_of(const AttnArgs &g, const AttnPlace &q, const AttnCounts &n, int64_t whole,
-                                              int head, int kind) {
+// (n: the counts of the kernel that the query's entry is of, shared out among ctas)
+__device__ __forceinline__ AttnParts parts_of(const AttnArgs &g, const AttnPlace &q, const AttnCounts &n, int ctas,
+                                              int64_t whole, int head, int kind) {
     AttnParts p = {};
     if (q.units == 0) return p;
     const bool many = q.many != 0;
-    const int ctas = ctas_of(n.units, many ? g.many_ctas : g.few_ctas), cost = many ? kManyCost : kFewCost;
+    const int cost = many ? kManyCost : kFewCost;
     const int kv = head / g.G, row = q.place * g.G + (head - kv * g.G);
     const int rows = many ? 128 * kManyTiles : kFewRows;
     const int seg = many ? kv : kv * q.tiles + row / kFewRows;
@@ -434,8 +437,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
         const int s = static_cast<int>((first + lane) / g.Hq), head = static_cast<int>((first + lane) - static_cast<int64_t>(s) * g.Hq);
         const AttnCounts many = *g.many, few = *g.few;
         const AttnPlace qa = g.places[s], qb = g.places[g.S + s];
-        a = parts_of(g, qa, qa.many != 0 ? many : few, first + lane, head, 0);
-        b = parts_of(g, qb, few, first + lane, head, 1);
+        const int fc = few_ctas_of(g, few.units), mc = many_ctas_of(g, many.units, few.units);
+        a = parts_of(g, qa, qa.many != 0 ? many : few, qa.many != 0 ? mc : fc, first + lane, head, 0);
+        b = parts_of(g, qb, few, fc, first + lane, head, 1);
     }
     for (int i = 0; i < each && first + i < rows; ++i) {
         const AttnParts pa = a.from(i), pb = b.from(i);
@@ -458,8 +462,8 @@ constexpr int kBorderRows = 8;   // CTAs of the rows of a border of the kernel f
 
 template <typename C, int D, int KEYS, int COST, bool FEW>
 __device__ __forceinline__ void join_border(const AttnArgs &g, int c, int part, int lane, int warp) {
-    const AttnCounts n = FEW ? *g.few : *g.many;
-    const int ctas = ctas_of(n.units, FEW ? g.few_ctas : g.many_ctas);
+    const AttnCounts many = *g.many, few = *g.few, n = FEW ? few : many;
+    const int ctas = FEW ? few_ctas_of(g, few.units) : many_ctas_of(g, many.units, few.units);
     if (c + 1 >= ctas) return;
     const int64_t *start = FEW ? g.few_start : g.many_start;
     const int64_t border = units_before(n.units, ctas, c + 1);
@@ -581,7 +585,7 @@ bool encode(CUtensorMap *map, int dtype, const void *base, int rank, const cuuin
 }
 
 template <typename C, int D>
-int launch_attn(const q4_prefix_attn_t &a, const AttnArgs &g, cudaStream_t stream) {
+int launch_attn(const q4_prefix_attn_t &a, AttnArgs &g, cudaStream_t stream) {
     const q4_kv_cache_t &c = a.cache;
     // (a stride that nothing steps over still has to be one that a map takes)
     auto bytes = [&](int64_t stride, int64_t count) { return static_cast<cuuint64_t>(count > 1 ? 2 * stride : 2 * D); };
@@ -615,6 +619,7 @@ int launch_attn(const q4_prefix_attn_t &a, const AttnArgs &g, cudaStream_t strea
     const bool few = a.own_lens != nullptr || g.many_ctas == 0 || a.groups > 1 || a.group_offsets != nullptr;
     if (few) {
         using F = FewAttn<D>;
+        g.beside_many = g.many_ctas > 0;
         static_assert(2 * (F::smem() + 1024) <= 228 * 1024, "two CTAs of an SM");
         static std::atomic<bool> configured[64];
         if ((st = allow_smem(attn_few_kernel<C, D>, F::smem(), configured)) != Q4_OK) return st;
