@@ -24,6 +24,8 @@ bool outputs_clash(const Span *out, int nout, const Span *in, int nin) {
 
 // Sizes and strides whose products stay far from 2^63.
 bool small(int64_t v) { return v >= 0 && v < (1ll << 44); }
+// Rows whose last one lies as near.
+bool small_rows(int64_t n, int64_t stride) { return n <= 1 || stride < (1ll << 44) / (n - 1); }
 
 // The pools of a cache: sizes that make sense, and the elements from the first to the last.
 int cache_shape(const q4_kv_cache_t &c) {
@@ -43,6 +45,7 @@ int cache_shape(const q4_kv_cache_t &c) {
     for (int i : order) {
         if (count[i] <= 1) continue;
         if (stride[i] < within) return Q4_ERR_INVALID_ARG;
+        if (stride[i] > (1ll << 44) / count[i]) return Q4_ERR_UNSUPPORTED;
         within += stride[i] * (count[i] - 1);
         if (!small(within)) return Q4_ERR_UNSUPPORTED;
     }
@@ -96,7 +99,9 @@ int q4_rope_append_run(const q4_rope_append_t *args, const q4_run_options_t *opt
     if (!small(g.q_stride) || g.q_stride < (g.T > 1 ? qrow : 0)) return Q4_ERR_INVALID_ARG;
     if (keys && (!small(g.k_stride) || !small(g.v_stride) || (g.T > 1 && (g.k_stride < krow || g.v_stride < krow))))
         return Q4_ERR_INVALID_ARG;
-    if (c.D > kMaxHeadD || qrow + 2 * krow > 0x7fffffLL) return Q4_ERR_UNSUPPORTED;
+    if (c.D > kMaxHeadD || qrow + 2 * krow > 0x7fffffLL || !small_rows(g.T, g.q_stride) ||
+        (keys && (!small_rows(g.T, g.k_stride) || !small_rows(g.T, g.v_stride))))
+        return Q4_ERR_UNSUPPORTED;
     if (g.T == 0) return Q4_OK;
     if (g.q == nullptr || g.q_out == nullptr || (g.rot > 0 && (g.positions == nullptr || g.inv_freq == nullptr)) ||
         (keys && c.pages > 0 && (c.k == nullptr || c.v == nullptr)))
@@ -168,7 +173,7 @@ int q4_prefix_attn_run(const q4_prefix_attn_t *args, const q4_run_options_t *opt
     if (g.groups == 0 && !own) return Q4_ERR_INVALID_ARG;
     const int64_t qrow = static_cast<int64_t>(g.Hq) * c.D;
     if (!small(g.q_stride) || (g.S > 1 && g.q_stride < qrow)) return Q4_ERR_INVALID_ARG;
-    if (c.page < 16 || (c.page & (c.page - 1)) != 0 || c.pages > 0x7fffffffLL ||
+    if (c.page < 16 || (c.page & (c.page - 1)) != 0 || c.pages > 0x7fffffffLL || !small_rows(g.S, g.q_stride) ||
         static_cast<int64_t>(g.max_shared_pages) * c.page > 0x7fffffffLL ||
         static_cast<int64_t>(g.max_own_pages) * c.page > 0x7fffffffLL)
         return Q4_ERR_UNSUPPORTED;
@@ -221,6 +226,7 @@ int q4_beam_step_run(const float *logits, int64_t row_stride, const float *score
     if (!small(row_stride) || (rows > 1 && row_stride < V) || eos < -1 || eos >= V ||
         (finished_or_null != nullptr && eos < 0))
         return Q4_ERR_INVALID_ARG;
+    if (!small_rows(rows, row_stride)) return Q4_ERR_UNSUPPORTED;
     if (groups == 0) return Q4_OK;
     if (logits == nullptr || scores == nullptr || tokens == nullptr || parents == nullptr || out_scores == nullptr ||
         workspace == nullptr || workspace_bytes < q4_beam_step_workspace(groups, W, K, V))

@@ -226,3 +226,13 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu():
         q4.q4_beam_step_run(torch.zeros(2, 9), torch.zeros(1, 2), None, None, None, None)
     with pytest.raises(ValueError):
         q4.q4_beam_reorder_run(None, None, None, None, None, None, torch.zeros(1, 1, 1, 1, 2))
+
+
+def test_strides_whose_products_pass_64_bits_are_refused(L):
+    most = 2 ** 31 - 1
+    for name in ("q_stride", "k_stride", "v_stride"):
+        assert rope(L, T=most, **{name: 2 ** 43}) == UNS, name
+    assert attn(L, S=2 ** 20, q_stride=2 ** 43) == UNS
+    assert beam(L, groups=2 ** 26, W=32, stride=2 ** 43) == UNS
+    for c in (cache(pages=2 ** 60), cache(pages=2 ** 31 - 1, page_stride=2 ** 43)):
+        assert rope(L, c=c) == UNS and attn(L, c=c) == UNS
