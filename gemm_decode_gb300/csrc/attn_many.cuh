@@ -26,8 +26,8 @@
 // the copies of keys and values write there too.  The other 560 are the hand-overs between the
 // MMAs and the weights (weights without exponentials: 3050).  A segment's beginning and end cost
 // about 2.4 units: the first scores and weights, and the results out of tensor memory.
-// Measured (graphs): 256 queries x 32 heads by 27900 keys of 8 heads 97 us, 1.2 PFLOP/s (0.63 of
-// measured bf16); a causal prompt of 4096 tokens 150 us with plan and join, 0.9 PFLOP/s.
+// Measured (graphs): 256 queries x 32 heads by 27900 keys of 8 heads 94 us, 1.25 PFLOP/s (0.65 of
+// measured bf16); a causal prompt of 4096 tokens 147 us with plan and join, 0.93 PFLOP/s.
 // Results stored 16 bytes a lane instead of whole sectors: 26 us more for the prompt.
 #pragma once
 
