@@ -14,8 +14,9 @@
 // ends.  Two CTAs to an SM, three stages of 32 KB each (128 features).
 //
 // Measured (cold caches): own segments of 64 sequences, 768 keys on average, 8 heads of 128
-// (201 MB) 38 us, 5.3 TB/s, 0.78 of measured; of 256 sequences, 218 keys (228 MB) 49 us: there a
-// segment is four units, and its queries' loads and its join cost two.
+// (201 MB) 41 us, 4.9 TB/s, 0.72 of measured (38 without the fence before a stage is given back,
+// and wrong); of 256 sequences, 218 keys (228 MB) 53 us: there a segment is four units, and its
+// queries' loads and its join cost two.
 #pragma once
 
 #include "attn_common.cuh"
