@@ -100,6 +100,14 @@ __device__ __forceinline__ int clamp_len(int n, int most_pages, int page) {
     return n < 0 ? 0 : n > most ? static_cast<int>(most) : n;
 }
 
+// Units of a number of keys.  A table may name just below 2^31 tokens: the sum is unsigned, where
+// no such number passes the type.
+__host__ __device__ constexpr int units_of(int keys, int unit) {
+    return static_cast<int>((static_cast<uint32_t>(keys) + static_cast<uint32_t>(unit - 1)) / static_cast<uint32_t>(unit));
+}
+static_assert(units_of(0, kManyKeys) == 0 && units_of(1, kManyKeys) == 1 && units_of(129, kManyKeys) == 2, "units");
+static_assert(units_of(0x7fffffff, kManyKeys) == 1 << 24 && units_of(0x7fffffff, kFewKeys) == 1 << 25, "units");
+
 // CTAs that take part (each has a unit), the units that CTA c of them takes, and the CTA that
 // takes unit u.
 __device__ __forceinline__ int few_ctas_of(const AttnArgs &g, int64_t few) {
@@ -193,7 +201,7 @@ struct AttnWalk {
             const int4 raw = i < AttnHeld::kMost ? held->entry[i] : __ldcg(reinterpret_cast<const int4 *>(entries + entry));
             const int64_t from = at - (i < AttnHeld::kMost ? held->start[i] : __ldcg(start + entry));
             s.e = AttnEntry{raw.x, raw.y, raw.z, raw.w};
-            s.units = (s.e.keys + KEYS - 1) / KEYS;
+            s.units = units_of(s.e.keys, KEYS);
             const int each = s.units + COST, tiles = FEW ? (s.e.queries * G + kFewRows - 1) / kFewRows : 1;
             const int seg = static_cast<int>(quotient(from, each)), off = static_cast<int>(from - static_cast<int64_t>(seg) * each);
             const int take = static_cast<int>(min(static_cast<int64_t>(each - off), end - at));

@@ -233,7 +233,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
             }
             // keys that a row does not see
             const int first = min(limit[0], limit[1]);
-            if (__any_sync(~0u, key0 + 16 > first)) {
+            if (__any_sync(~0u, first - key0 < 16)) {   // (key0 + 16 may be 2^31)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -271,7 +271,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant
             }
             // values behind the segment's last key are not the sequence's: zeros, whatever they are
             uint32_t keep[2] = {~0u, ~0u};
-            const bool ragged = key0 + 16 > s.e.keys;
+            const bool ragged = s.e.keys - key0 < 16;
             if (ragged) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)

@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
             group = last_at_most(run_of, g.groups, r);
             keys = g.limits != nullptr ? run_keys[r] : group_len(group);
         }
-        const int64_t mine = keys > 0 ? static_cast<int64_t>((keys + kManyKeys - 1) / kManyKeys + kManyCost) * g.Hkv : 0;
+        const int64_t mine = keys > 0 ? static_cast<int64_t>(units_of(keys, kManyKeys) + kManyCost) * g.Hkv : 0;
         int64_t u = mine, tu;
         int e = keys > 0 ? 1 : 0, te;
         block_scan(u, e, tu, te, sa, sb);
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
             }
         }
         const int tiles = (a.queries * g.G + kFewRows - 1) / kFewRows;
-        const int units = (a.keys + kFewKeys - 1) / kFewKeys;
+        const int units = units_of(a.keys, kFewKeys);
         const int64_t mine = a.keys > 0 ? static_cast<int64_t>(units + kFewCost) * g.Hkv * tiles : 0;
         int64_t u = mine, tu;
         int e = a.keys > 0 ? 1 : 0, te;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
                 const int first = first_of[group];
                 if (few_group(first_of[group + 1] - first)) continue;
                 const int r = (s - first) / run, keys = run_keys[run_of[group] + r];
-                at.units = (keys + kManyKeys - 1) / kManyKeys;
+                at.units = units_of(keys, kManyKeys);
                 if (own) {
                     at.start = run_start[run_of[group] + r];
                     at.many = 1;
@@ -469,7 +469,7 @@ __device__ __forceinline__ void join_border(const AttnArgs &g, int c, int part, 
     const int64_t border = units_before(n.units, ctas, c + 1);
     const int entry = entry_at(start, n.entries, border, lane);
     const AttnEntry e = FEW ? g.few_entries[entry] : g.many_entries[entry];
-    const int units = (e.keys + KEYS - 1) / KEYS, each = units + COST;
+    const int units = units_of(e.keys, KEYS), each = units + COST;
     const int seg = static_cast<int>(quotient(border - start[entry], each));
     const int64_t u0 = start[entry] + static_cast<int64_t>(seg) * each + COST;   // its first unit
     const int count = owner_of(n.units, ctas, u0 + units - 1) - c + 1;
