@@ -186,13 +186,13 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_chunk_kernel(const BeamA
     extern __shared__ __align__(16) unsigned char beam_raw[];
     BeamShared &sh = *reinterpret_cast<BeamShared *>(beam_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.y, K = g.K;
+    const int row = blockIdx.x, K = g.K;   // (rows in the grid's first dimension: up to 2^31 of them)
     wait_prior_grid();
     allow_next_grid();
     const float cum = g.scores[row];
     if (!(fabsf(cum) <= kLargest) || (g.finished != nullptr && g.finished[row] != 0)) return;
     const float *l = g.logits + row * g.row_stride;
-    const int64_t v0 = blockIdx.x * chunk, v1 = v0 + chunk < g.V ? v0 + chunk : g.V;
+    const int64_t v0 = blockIdx.y * chunk, v1 = v0 + chunk < g.V ? v0 + chunk : g.V;
     const float none = -__int_as_float(0x7f800000);
     auto ib = [&](int64_t v, int n) {
         return q4_in_bounds(v >= 0 && v + n <= g.V && row < g.groups * g.W, g.bounds);
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_chunk_kernel(const BeamA
     for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(~0u, ws, o);
     if (lane == 0) sh.sums[warp] = make_float2(wm, ws);
     __syncthreads();
-    const int64_t slot = static_cast<int64_t>(row) * gridDim.x + blockIdx.x;
+    const int64_t slot = static_cast<int64_t>(row) * gridDim.y + blockIdx.y;
     if (threadIdx.x < K) keys[slot * K + threadIdx.x] = sh.kept[threadIdx.x];
     if (threadIdx.x == 32) {
         float am = sh.sums[0].x, as = 0.0f;
@@ -480,22 +480,12 @@ int launch_beam_step(const BeamArgs &a, cudaStream_t stream) {
     const int wide = aligned(a.logits, 16) && a.row_stride % 4 == 0;
     static_assert(sizeof(BeamShared) <= 48 * 1024, "shared memory without asking for more");
     const bool overlap = call_options().overlap;
-    // the grid's second dimension has 65535 places
-    for (int r0 = 0; r0 < rows; r0 += 65535 / a.W * a.W) {
-        BeamArgs p = a;
-        const int part = rows - r0 < 65535 / a.W * a.W ? rows - r0 : 65535 / a.W * a.W;
-        p.logits += static_cast<int64_t>(r0) * a.row_stride;
-        p.scores += r0;
-        if (p.finished != nullptr) p.finished += r0;
-        const int st = launch_overlappable(beam_chunk_kernel, dim3(static_cast<unsigned>(b.chunks), static_cast<unsigned>(part)),
-                                           dim3(kBeamThreads), sizeof(BeamShared), stream, overlap, p, b.chunk, wide,
-                                           stats + static_cast<int64_t>(r0) * b.chunks,
-                                           keys + static_cast<int64_t>(r0) * b.chunks * a.K);
-        if (st != Q4_OK) return st;
-    }
+    int st = launch_overlappable(beam_chunk_kernel, dim3(static_cast<unsigned>(rows), static_cast<unsigned>(b.chunks)),
+                                 dim3(kBeamThreads), sizeof(BeamShared), stream, overlap, a, b.chunk, wide, stats, keys);
+    if (st != Q4_OK) return st;
     const size_t lists = static_cast<size_t>(kJoinWarps) * b.chunks * a.K * sizeof(uint64_t);   // at most 128 KB
     static std::atomic<bool> configured[64];
-    const int st = allow_smem(beam_join_kernel, kJoinWarps * kMaxChunks * kMaxBeams * sizeof(uint64_t), configured);
+    st = allow_smem(beam_join_kernel, kJoinWarps * kMaxChunks * kMaxBeams * sizeof(uint64_t), configured);
     if (st != Q4_OK) return st;
     return launch_overlappable(beam_join_kernel, dim3(static_cast<unsigned>(a.groups)), dim3(32 * kJoinWarps), lists,
                                stream, true, a, b.chunks, stats, keys);
