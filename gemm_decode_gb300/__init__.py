@@ -872,7 +872,7 @@ def q4_prefix_attn_run(q, k_cache, v_cache, out, workspace, group_offsets=None, 
 
 
 def q4_beam_step_workspace(groups, W, K, V) -> int:
-    """Bytes of workspace q4_beam_step_run needs."""
+    """Bytes of workspace q4_beam_step_run needs on the current device."""
     return _workspace(lib().q4_beam_step_workspace(int(groups), int(W), int(K), int(V)), "q4_beam_step_workspace")
 
 

@@ -29,18 +29,18 @@ constexpr int kBeamThreads = 256;
 constexpr int kPerThread = 16;
 constexpr int kBlock = kBeamThreads * kPerThread;   // logits in registers at a time
 constexpr int kMaxChunks = 64;                      // of one beam
-constexpr int kChunkCtas = 608;                     // chunks wanted: four to an SM
+constexpr int kChunkCtas = 4;                       // of an SM: chunks wanted
 
 // What a chunk leaves: maximum, sum of exponentials, and keys.
 struct BeamLayout {
     int chunks;
     int64_t chunk;   // logits
 };
-// As many chunks as CTAs are resident at a time, so that there is one wave of them; a block at
-// least to a chunk.
+// As many chunks as CTAs are resident on the current device at a time, so that there is one wave of
+// them; a block at least to a chunk.
 BeamLayout beam_layout(int64_t rows, int64_t V) {
     const int64_t blocks = (V + kBlock - 1) / kBlock;
-    const int64_t want = std::min({blocks, std::max<int64_t>(kChunkCtas / std::max<int64_t>(rows, 1), 1),
+    const int64_t want = std::min({blocks, std::max<int64_t>(kChunkCtas * device_info().sms / std::max<int64_t>(rows, 1), 1),
                                    static_cast<int64_t>(kMaxChunks)});
     const int64_t chunk = ((V + want - 1) / want + 31) / 32 * 32;   // (chunks start where rows of 16 bytes do)
     return BeamLayout{static_cast<int>((V + chunk - 1) / chunk), chunk};
@@ -181,7 +181,7 @@ struct BeamShared {
 };
 constexpr int kFew = (kWarps * (kLong + kBatch * kPerThread) - kMaxBeams) / kPerThread;   // sixteens whose keys all have room
 
-__global__ void __launch_bounds__(kBeamThreads, 4) beam_chunk_kernel(const BeamArgs g, int64_t chunk, int wide,
+__global__ void __launch_bounds__(kBeamThreads, kChunkCtas) beam_chunk_kernel(const BeamArgs g, int64_t chunk, int wide,
                                                                      float2 *stats, uint64_t *keys) {
     extern __shared__ __align__(16) unsigned char beam_raw[];
     BeamShared &sh = *reinterpret_cast<BeamShared *>(beam_raw);

@@ -600,7 +600,8 @@ Q4_API int64_t q4_prefix_attn_workspace(int32_t S, int32_t groups, int32_t Hq, i
  * is an empty problem.  Q4_ERR_TIMEOUT from q4gemv_device_status if a bounded wait expired. */
 Q4_API int q4_prefix_attn_run(const q4_prefix_attn_t *args, const q4_run_options_t *opts, void *stream);
 
-/* Bytes of workspace q4_beam_step_run needs (-1 for sizes it does not serve). */
+/* Bytes of workspace q4_beam_step_run needs on the current device (-1 for sizes it does not
+ * serve). */
 Q4_API int64_t q4_beam_step_workspace(int32_t groups, int32_t W, int32_t K, int64_t V);
 
 /* One step of a beam search: the K best continuations of each group of W beams.

@@ -4,6 +4,8 @@ import pytest
 from gpu_util import torch_cuda
 from test_gpu_beam import step
 
+import gemm_decode_gb300 as q4
+
 pytestmark = pytest.mark.gpu
 
 
@@ -62,3 +64,15 @@ def test_chunks_of_several_parts(torch, rows, W, K, V):
     for p in part:
         want = by_definition(torch, logits[p.start * W:p.stop * W], scores[p], K)
         same(torch, [t[p] for t in got[:3]], want, V)
+
+
+def test_chunks_follow_the_device(torch):
+    """One row is split into as many chunks as there are blocks of 4096 logits, up to 64, and many
+    rows into so many that four CTAs an SM have one each; a chunk leaves K keys and two sums."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for rows, K, V in ((1, 4, 4097), (1, 1, 10 ** 6), (64, 8, 128256), (sms, 2, 50000), (4 * sms, 3, 50000), (5 * sms, 1, 9000)):
+        blocks = -(-V // 4096)
+        want = min(blocks, max(4 * sms // rows, 1), 64)
+        chunk = -(-(-(-V // want)) // 32) * 32
+        bytes_ = rows * -(-V // chunk) * (8 + 8 * K)
+        assert q4.q4_beam_step_workspace(rows, 1, K, V) == -(-bytes_ // 256) * 256 + 256
