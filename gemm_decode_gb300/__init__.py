@@ -880,7 +880,8 @@ def q4_beam_step_run(logits, scores, tokens, parents, out_scores, workspace, fin
                      flags=None, stream=None, check=True) -> int:
     """The K best continuations of each group: tokens, parents, out_scores (and out_finished,
     uint8) [groups, K] from logits [groups * W, V] (rows may be any stride apart) and the
-    beams' scores (and finished, uint8) [groups, W]."""
+    beams' scores (and finished, uint8) [groups, W].  The order within a beam is that of its
+    logits, then tokens; between beams that of the scores, then beams."""
     dev = _device(logits, "logits")
     rows, V = logits.shape
     groups, W = scores.shape

@@ -437,9 +437,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) beam_join_kernel(const BeamAr
         __syncwarp();
     }
     __syncthreads();
-    // The places are in the order of beams, and within a beam of scores, then tokens: of equal
-    // scores the lower place is the one with the lower beam, then the lower token.  A candidate's
-    // place among the chosen is the number of better ones.
+    // The places are in the order of beams, and within a beam of logits, then tokens: the order of
+    // its exact scores, also of two that round to one binary64 number.  Of equal scores the lower
+    // place is the one with the lower beam.  A candidate's place among the chosen is the number of
+    // better ones.
     const int n = g.W * K;
     if (threadIdx.x < K) {   // for places that nothing fills
         const int64_t to = static_cast<int64_t>(group) * K + threadIdx.x;

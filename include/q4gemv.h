@@ -610,8 +610,11 @@ Q4_API int64_t q4_beam_step_workspace(int32_t groups, int32_t W, int32_t K, int6
  * finished[g][w] != 0 has one continuation, token eos at its own score.  NaN and infinite
  * logits count as -inf and are never chosen; a beam whose score is not finite has no
  * continuation.  Places left over hold token -1, parent -1, score -inf, finished 0.
- * The order is that of the scores before they are rounded to binary32 (sums of exponentials
- * in binary32, logarithms and scores in binary64).
+ * The continuations of one beam are in the order of their logits, exactly, equal logits by lower
+ * v: also where the logits are so close, or the beam's score so large, that the scores round to
+ * the same number.  Those of different beams are in the order of the scores as they are formed
+ * (sums of exponentials in binary32, logarithms and scores in binary64), before they are rounded
+ * to binary32.
  *   logits : device float [groups W][V], row r at r * row_stride;  scores : device float
  *   [groups][W];  finished_or_null : device uint8 [groups][W] (eos >= 0 then);
  *   eos : a token, or -1

@@ -76,3 +76,32 @@ def test_chunks_follow_the_device(torch):
         chunk = -(-(-(-V // want)) // 32) * 32
         bytes_ = rows * -(-V // chunk) * (8 + 8 * K)
         assert q4.q4_beam_step_workspace(rows, 1, K, V) == -(-bytes_ // 256) * 256 + 256
+
+
+def test_logits_whose_scores_round_alike(torch):
+    """Within a beam the order is that of the logits, then the tokens, where binary64 scores are
+    equal: logits far below the score's last bit, and beams' scores that swallow them."""
+    V = 6000
+    logits = torch.full((1, V), -20.0, device="cuda")
+    at = [4100, 17, 5999, 2500]
+    for i, v in enumerate(at):
+        logits[0, v] = (i + 1) * 1e-17          # binary64 keeps 1e-16 of a score of some units
+    logits[0, 40], logits[0, 30] = 4e-17, 2e-17   # as large as the last and the second
+    zero = torch.zeros(1, 1, device="cuda")
+    got = step(torch, logits, zero, 6)
+    assert float(logits[0, 40]) == float(logits[0, 2500]) and float(logits[0, 30]) == float(logits[0, 17])
+    assert got[0].tolist() == [[40, 2500, 5999, 17 if 17 < 30 else 30, 30, 4100]]
+    assert step(torch, logits, zero, 2)[0].tolist() == [[40, 2500]]
+    # two beams so far down that no logit moves their scores: the lower beam's logits in order
+    logits = torch.randn(2, V, device="cuda")
+    want = torch.sort(logits[0].double().cpu(), descending=True, stable=True).indices[:5].tolist()
+    got = step(torch, logits, torch.full((1, 2), -1e30, device="cuda"), 5)
+    assert got[0].tolist() == [want] and got[1].tolist() == [[0] * 5]
+    # a finished beam beside a live one whose best continuation scores nearly the same
+    logits = torch.full((2, V), -60.0, device="cuda")
+    logits[1, 9] = 0.0                           # that beam's sum is 1 + 5999 e^-60: its best scores its own score
+    done = torch.tensor([[1, 0]], device="cuda", dtype=torch.uint8)
+    for first, parent in ((-1.0, 0), (-1.0 - 2.0 ** -20, 1)):
+        got = step(torch, logits, torch.tensor([[first, -1.0]], device="cuda"), 2, finished=done, eos=3)
+        assert got[1].tolist() == [[parent, 1 - parent]]
+        assert got[0].tolist() == [[3, 9] if parent == 0 else [9, 3]] and got[3].tolist() == [[1, 0] if parent == 0 else [0, 1]]
