@@ -48,6 +48,9 @@ struct ManyAttn {
     static constexpr int kStages = D == 128 ? 5 : 8;
     static constexpr int kBars = 2 * kStages + 14;   // (an even number: what follows is aligned to 16 bytes)
     static constexpr int kTmemCols = 512;
+    // Registers that the roles have after the hand-over: a block launched with fewer would wait for
+    // them without end, so the launch is refused where the kernel was not compiled to have them.
+    static constexpr int kRegisters = 128 * 88 + 256 * 208;
     static constexpr size_t smem() {
         return 1024 + static_cast<size_t>(kManyTiles + kStages) * kTileBytes + 8 * kBars + sizeof(AttnHeld) + 16;
     }

@@ -584,6 +584,24 @@ bool encode(CUtensorMap *map, int dtype, const void *base, int rank, const cuuin
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether a kernel was compiled to have `registers` with `threads` a block, looked up once per device.
+template <typename... P>
+int has_registers(void (*kernel)(P...), int threads, int registers, std::atomic<bool> *known) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && known[dev]) return Q4_OK;
+    cudaFuncAttributes a = {};
+    const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        set_cuda_error(e);
+        return Q4_ERR_CUDA;
+    }
+    if (a.numRegs * threads < registers) return Q4_ERR_UNSUPPORTED;
+    if (dev >= 0 && dev < 64) known[dev] = true;
+    return Q4_OK;
+}
+
 template <typename C, int D>
 int launch_attn(const q4_prefix_attn_t &a, AttnArgs &g, cudaStream_t stream) {
     const q4_kv_cache_t &c = a.cache;
@@ -604,6 +622,8 @@ int launch_attn(const q4_prefix_attn_t &a, AttnArgs &g, cudaStream_t stream) {
     if (st != Q4_OK) return st;
     if (g.many_ctas > 0) {
         using M = ManyAttn<D>;
+        static std::atomic<bool> known[64];
+        if ((st = has_registers(attn_many_kernel<C, D>, M::kThreads, M::kRegisters, known)) != Q4_OK) return st;
         static_assert(M::smem() <= 227 * 1024, "shared memory of one CTA");
         static std::atomic<bool> configured[64];
         if ((st = allow_smem(attn_many_kernel<C, D>, M::smem(), configured)) != Q4_OK) return st;
