@@ -615,34 +615,39 @@ int launch_attn(const q4_prefix_attn_t &a, AttnArgs &g, cudaStream_t stream) {
     CUtensorMap map_k, map_v, map_q;
     if (!encode(&map_k, c.dtype, c.k, 4, dims, strides, box) || !encode(&map_v, c.dtype, c.v, 4, dims, strides, box))
         return Q4_ERR_UNSUPPORTED;
-    // no more warps than there are queries or groups: each barrier costs by the warp
-    const int places = std::max(a.S, a.groups + 1);
-    const unsigned threads = static_cast<unsigned>(std::min(kPlanThreads, (places + 31) / 32 * 32));
-    int st = launch_overlappable(attn_plan_kernel, dim3(1), dim3(threads), 0, stream, call_options().overlap, g);
-    if (st != Q4_OK) return st;
+    using M = ManyAttn<D>;
+    using F = FewAttn<D>;
+    static_assert(M::smem() <= 227 * 1024, "shared memory of one CTA");
+    static_assert(2 * (F::smem() + 1024) <= 228 * 1024, "two CTAs of an SM");
+    // (no own segments and one group: all its queries have more than 16 rows, or all are few)
+    const bool few = a.own_lens != nullptr || g.many_ctas == 0 || a.groups > 1 || a.group_offsets != nullptr;
+    int st = Q4_OK;
+    // whatever can be refused, before anything is launched
     if (g.many_ctas > 0) {
-        using M = ManyAttn<D>;
-        static std::atomic<bool> known[64];
+        static std::atomic<bool> known[64], configured[64];
         if ((st = has_registers(attn_many_kernel<C, D>, M::kThreads, M::kRegisters, known)) != Q4_OK) return st;
-        static_assert(M::smem() <= 227 * 1024, "shared memory of one CTA");
-        static std::atomic<bool> configured[64];
         if ((st = allow_smem(attn_many_kernel<C, D>, M::smem(), configured)) != Q4_OK) return st;
         const cuuint64_t qd[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.S)};
         const cuuint64_t qs[2] = {2 * D, bytes(a.q_stride, a.S)};
         const cuuint32_t qb[3] = {64, static_cast<cuuint32_t>(g.G), static_cast<cuuint32_t>(g.tile_queries)};
         if (!encode(&map_q, c.dtype, a.q, 3, qd, qs, qb)) return Q4_ERR_UNSUPPORTED;
+    }
+    if (few) {
+        static std::atomic<bool> configured[64];
+        if ((st = allow_smem(attn_few_kernel<C, D>, F::smem(), configured)) != Q4_OK) return st;
+    }
+    // no more warps than there are queries or groups: each barrier costs by the warp
+    const int places = std::max(a.S, a.groups + 1);
+    const unsigned threads = static_cast<unsigned>(std::min(kPlanThreads, (places + 31) / 32 * 32));
+    st = launch_overlappable(attn_plan_kernel, dim3(1), dim3(threads), 0, stream, call_options().overlap, g);
+    if (st != Q4_OK) return st;
+    if (g.many_ctas > 0) {
         st = launch_overlappable(attn_many_kernel<C, D>, dim3(static_cast<unsigned>(g.many_ctas)), dim3(M::kThreads),
                                  M::smem(), stream, true, map_q, map_k, map_v, g);
         if (st != Q4_OK) return st;
     }
-    // (no own segments and one group: all its queries have more than 16 rows, or all are few)
-    const bool few = a.own_lens != nullptr || g.many_ctas == 0 || a.groups > 1 || a.group_offsets != nullptr;
     if (few) {
-        using F = FewAttn<D>;
         g.beside_many = g.many_ctas > 0;
-        static_assert(2 * (F::smem() + 1024) <= 228 * 1024, "two CTAs of an SM");
-        static std::atomic<bool> configured[64];
-        if ((st = allow_smem(attn_few_kernel<C, D>, F::smem(), configured)) != Q4_OK) return st;
         st = launch_overlappable(attn_few_kernel<C, D>, dim3(static_cast<unsigned>(g.few_ctas)), dim3(F::kThreads),
                                  F::smem(), stream, true, map_k, map_v, g);
         if (st != Q4_OK) return st;

@@ -49,3 +49,21 @@ def test_tables_of_the_most_tokens(torch, kind):
     ref.within(out, want, (v.abs().sum((0, 1, 2)) / n * (2 * steps + 80 * 2.0 ** -24)).expand(S, 1, D), "out")
     log = torch.full((S, 1), math.log(n * times), dtype=torch.float64)
     ref.within(lse, log, steps + 4 * 2.0 ** -24 * log, "lse")
+
+
+def test_a_refused_call_launches_nothing(torch):
+    """Rows of queries too far apart for a tensor map are refused before the plan is written."""
+    p = attn.problem(torch, [20], [40], None, 8, 2, 64, 16, torch.bfloat16)
+    S, Hq, D = p["q"].shape
+    ws = torch.full((q4.q4_prefix_attn_workspace(S, 1, Hq, 2, D),), 255, device="cuda", dtype=torch.uint8)
+    out = torch.full((S, Hq, D), 9.0, device="cuda", dtype=torch.bfloat16)
+    far = 1 << 50   # an address that nothing else of the call is near; never read
+    cache = q4._cache(0, p["k_cache"], p["v_cache"])
+    a = q4._ATTN.pack(S, Hq, 1, q4.Q4_BF16, p["shared_pages"].shape[1], 0, 0.1, far, 2 ** 39, *cache, 0,
+                      p["shared_pages"].data_ptr(), p["shared_lens"].data_ptr(), 0, 0, 0, out.data_ptr(), 0, ws.data_ptr(),
+                      ws.numel())
+    assert q4.lib().q4_prefix_attn_run(a, None, None) == q4.Q4_ERR_UNSUPPORTED
+    torch.cuda.synchronize()
+    assert (ws == 255).all() and (out == 9).all()
+    check = attn.check(torch, p, ws=ws)   # and the call after it is right
+    assert torch.isfinite(check[0]).all()
