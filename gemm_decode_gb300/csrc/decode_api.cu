@@ -258,7 +258,7 @@ int q4_beam_reorder_run(const q4_beam_reorder_t *args, const q4_run_options_t *o
         !small(g.page_stride) || !small(g.head_stride) || !small(g.row_stride))
         return Q4_ERR_INVALID_ARG;
     const int64_t n = static_cast<int64_t>(g.groups) * g.W;
-    if (g.W > kMaxReorderW || n > 0x7fffffffLL || g.pages > 0x7fffffffLL ||
+    if (g.W > kMaxReorderW || n > 0x7fffffffLL || g.pages > 0x7fffffffLL || !small_rows(n + 1, g.max_pages) ||
         static_cast<int64_t>(g.heads) * g.page > 0x7fffffffLL / g.row_bytes)
         return Q4_ERR_UNSUPPORTED;
     int64_t bytes = 0;

@@ -660,8 +660,8 @@ typedef struct {
  * A parent outside [0, W) counts as the sequence itself; pages outside [0, pages) are neither
  * read nor written; lens are clamped to [0, max_pages * page] (at max_pages * page there is no
  * page being written).  out_tables and out_spare may not overlap tables and spare.
- * pool and strides 2-byte aligned, row_bytes even.  groups W < 2^31 (Q4_ERR_UNSUPPORTED above),
- * 1 <= W <= 1024.  groups == 0 is an empty problem. */
+ * pool and strides 2-byte aligned, row_bytes even.  groups W < 2^31, tables of fewer than 2^44
+ * entries (Q4_ERR_UNSUPPORTED above), 1 <= W <= 1024.  groups == 0 is an empty problem. */
 Q4_API int q4_beam_reorder_run(const q4_beam_reorder_t *args, const q4_run_options_t *opts, void *stream);
 
 /* ---- test and measurement exports (not part of the GEMV API proper) ---------------- */
