@@ -782,7 +782,7 @@ def _heads(dev, t, name, T, H, D, dtype):
 def q4_rope_append_run(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slots=None, q_gamma=None, k_gamma=None,
                        eps=1e-6, layout=Q4_ROPE_HALF, scale=1.0, flags=None, stream=None, check=True) -> int:
     """Norm and rotary positions of q [T, Hq, D] into q_out, and of k [T, Hkv, D] into the
-    cache, with v, at slots [T] (None: token t at slot t).  The heads of a token lie side by
+    cache, with v, at slots [T] (None: token t at slot t; no two the same, or -1).  The heads of a token lie side by
     side; tokens may be any stride apart, so q, k and v may be parts of one product's rows.
     k and v None: queries only (k_cache, v_cache None too).  inv_freq [rot / 2] float32:
     2 len(inv_freq) features are rotated."""

@@ -528,8 +528,8 @@ typedef struct {
  * binary32, rounded once when stored.  The angle is reduced exactly (a product of integers
  * modulo one turn), so a far position costs no accuracy: cosines and sines are within 2^-21
  * for any int32 position and |inv_freq| <= 16.
- * A slot outside [0, pages * page) (-1: a padding token) is not written; of two tokens with
- * the same slot either may stay.  inv_freq, gammas, positions and slots 4-byte aligned, q, k,
+ * A slot outside [0, pages * page) (-1: a padding token) is not written; tokens with the same
+ * slot leave a row each of whose elements is one of theirs, not all of the same one.  inv_freq, gammas, positions and slots 4-byte aligned, q, k,
  * v and the pools to their elements.  1 <= D <= 256 (Q4_ERR_UNSUPPORTED above).  T == 0 is
  * an empty problem. */
 Q4_API int q4_rope_append_run(const q4_rope_append_t *args, const q4_run_options_t *opts, void *stream);
