@@ -90,11 +90,6 @@ struct AttnArgs {
 };
 
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ int clamp_len(int n, int most_pages, int page) {
     const int64_t most = static_cast<int64_t>(most_pages) * page;   // below 2^31: checked by the call
     return n < 0 ? 0 : n > most ? static_cast<int>(most) : n;
@@ -241,12 +236,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
             "r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
-}
-template <typename C>
-__device__ __forceinline__ C from_f32(float v) {
-    if constexpr (std::is_same<C, __half>::value) return __float2half_rn(v);
-    else if constexpr (std::is_same<C, __nv_bfloat16>::value) return __float2bfloat16_rn(v);
-    else return v;
 }
 template <typename C>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {   // a in the lower half

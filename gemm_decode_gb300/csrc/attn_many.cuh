@@ -148,11 +148,6 @@ __device__ __forceinline__ void tmem_ld<128>(uint32_t addr, float *f) {
         : "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 // 32 bytes of a row, a sector in one go where it is aligned (each lane has a row of its own).
 __device__ __forceinline__ void put32(void *to, const uint32_t *w, bool wide) {
     if (wide) {

@@ -49,17 +49,7 @@ BeamLayout beam_layout(int64_t rows, int64_t V) {
 constexpr float kLargest = 3.402823466e38f;
 
 // exp(x), x <= 0, within 2^-21: the product and the function each within 2^-23 and a half
-__device__ __forceinline__ float exp2_of(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float exp_of(float x) { return exp2_of(x * 1.44269504088896341f); }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
+__device__ __forceinline__ float exp_of(float x) { return exp2_fast(x * 1.44269504088896341f); }
 
 // Larger logit first, then lower token; 0: no logit.  (l + 0: both zeros are one value.)
 __device__ __forceinline__ uint64_t key_of(float l, uint32_t token) {
@@ -251,7 +241,7 @@ __global__ void __launch_bounds__(kBeamThreads, kChunkCtas) beam_chunk_kernel(co
 #pragma unroll
                 for (int i = 0; i < kPerThread; i += 2) {
                     const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), minus), log2e);
-                    sum = __fadd2_rn(sum, make_float2(exp2_of(y.x), exp2_of(y.y)));
+                    sum = __fadd2_rn(sum, make_float2(exp2_fast(y.x), exp2_fast(y.y)));
                 }
                 part = sum.x + sum.y;
             };

@@ -14,6 +14,17 @@ constexpr int kMaxReorderW = 1024;
 constexpr int kMaxQueries = 1 << 20;
 constexpr int kMaxShare = 128;      // query heads of a kv head
 
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // The dynamic shared memory that a kernel may be launched with, set once per device.
 template <typename... P>
 int allow_smem(void (*kernel)(P...), size_t bytes, std::atomic<bool> *configured) {

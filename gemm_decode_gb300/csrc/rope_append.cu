@@ -23,7 +23,6 @@
 // and four tokens to a CTA with the next one's rows on their way (32 us), gained nothing.
 #include <cuda_bf16.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "q4_decode.cuh"
