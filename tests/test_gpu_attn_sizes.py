@@ -67,3 +67,92 @@ def test_a_refused_call_launches_nothing(torch):
     assert (ws == 255).all() and (out == 9).all()
     check = attn.check(torch, p, ws=ws)   # and the call after it is right
     assert torch.isfinite(check[0]).all()
+
+
+def ragged(n, most):
+    """Sizes of n groups, 0 to `most`, empty ones side by side and at both ends."""
+    return [0, 0] + [(7 * g + g // 5) % (most + 1) for g in range(n - 4)] + [0, 0]
+
+
+def with_limits(torch, p, kind):
+    if kind == "limits":
+        S = p["q"].shape[0]
+        limits = torch.randint(-2, 70, (S,), device="cuda")
+        limits[::17] = 0
+        p["limits"] = limits.to(torch.int32)
+    return p
+
+
+# groups in one warp's lanes up to 31, in shared memory up to 1024, in the workspace beyond
+GROUPS = [(31, 20, 4, 2), (32, 20, 4, 2), (33, 3, 4, 2), (130, 9, 4, 2), (1023, 3, 8, 1), (1024, 3, 8, 1), (1025, 3, 8, 1),
+          (2050, 3, 16, 1)]   # (no more groups than queries: others are refused)
+
+
+@pytest.mark.parametrize("kind", ["plain", "limits"])
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("groups,most,Hq,Hkv", GROUPS)
+def test_numbers_of_groups(torch, groups, most, Hq, Hkv, own, kind):
+    sizes = ragged(groups, most)
+    S = sum(sizes)
+    shared = [(11 * g) % 67 for g in range(groups)]
+    p = attn.problem(torch, sizes, shared, [(5 * s) % 23 for s in range(S)] if own else None, Hq, Hkv, 64, 16,
+                     torch.bfloat16, stale=groups < 200)
+    attn.check(torch, with_limits(torch, p, kind))
+
+
+@pytest.mark.parametrize("kind", ["plain", "limits"])
+@pytest.mark.parametrize("sizes,own", [([2100], False), ([2100], True), ([3] * 700, False), ([3, 0, 5, 1] * 250, True)])
+def test_numbers_of_runs(torch, sizes, own, kind):
+    """Two queries a run (128 query heads of a kv head): more runs than shared memory holds."""
+    S = sum(sizes)
+    p = attn.problem(torch, sizes, [40 + g % 30 for g in range(len(sizes))], [s % 9 for s in range(S)] if own else None,
+                     128, 1, 64, 16, torch.float16, stale=False)
+    attn.check(torch, with_limits(torch, p, kind))
+
+
+def test_many_segments_a_cta(torch):
+    """More than the 32 entries that a CTA holds in shared memory, in both kernels."""
+    S = 12000
+    p = attn.problem(torch, [S], None, [1 + (13 * s) % 40 for s in range(S)], 1, 1, 64, 16, torch.bfloat16, stale=False)
+    attn.check(torch, p)
+    S = 6000
+    p = attn.problem(torch, [1] * S, [1 + (29 * s) % 90 for s in range(S)], None, 32, 1, 64, 16, torch.bfloat16, stale=False)
+    attn.check(torch, p)
+    attn.check(torch, with_limits(torch, p, "limits"))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 1, 64), (14, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("queries", [1, 3, 20, 90])
+def test_rows_of_many_parts(torch, queries, Hq, Hkv, D):
+    """A long segment is shared by all CTAs: a row has parts by the hundred, joined 32 at a time."""
+    n = 30011
+    one = attn.problem(torch, [queries], [n], None, Hq, Hkv, D, 64, torch.bfloat16)
+    attn.check(torch, one)                                                   # shared segments alone
+    one["limits"] = torch.linspace(1, n, queries, device="cuda").to(torch.int32)
+    attn.check(torch, one)
+    attn.check(torch, attn.problem(torch, [queries], [n], [9000 + s for s in range(min(queries, 3))] + [3] * (queries - min(queries, 3)),
+                                   Hq, Hkv, D, 64, torch.float16))           # both kinds
+    if queries <= 3:
+        attn.check(torch, attn.problem(torch, [queries], None, [n - s for s in range(queries)], Hq, Hkv, D, 64, torch.bfloat16))
+
+
+def test_waits_of_any_bound_end(torch):
+    """Whatever a wait's bound, the call ends: with the right result, or with a status that says
+    that a wait gave up, after which a call in the same workspace is right."""
+    for case in (dict(sizes=[70, 2], shared=[3000, 500], own=[200] * 72), dict(sizes=[300], shared=[700], own=None),
+                 dict(sizes=[6], shared=None, own=[5000] * 6)):
+        p = attn.problem(torch, case["sizes"], case["shared"], case["own"], 8, 2, 128, 16, torch.bfloat16)
+        S, groups = p["q"].shape[0], len(case["shared"] or [])
+        ws = torch.empty(q4.q4_prefix_attn_workspace(S, groups, 8, 2, 128), device="cuda", dtype=torch.uint8)
+        right, lse = attn.check(torch, p, ws=ws)
+        ended = set()
+        for bound in (0, 1, 100, 1000, 3000, 10000, 10 ** 9):
+            out, l = attn.run(torch, p, ws=ws, wait_timeout_ns=bound)
+            status = q4.q4gemv_device_status()
+            assert status in (q4.Q4_OK, q4.Q4_ERR_TIMEOUT)
+            ended.add(status)
+            if status == q4.Q4_OK:
+                assert torch.equal(out, right) and torch.equal(l, lse)
+            out, l = attn.run(torch, p, ws=ws)
+            assert q4.q4gemv_device_status() == q4.Q4_OK and torch.equal(out, right) and torch.equal(l, lse)
+        assert ended == {q4.Q4_OK, q4.Q4_ERR_TIMEOUT}
