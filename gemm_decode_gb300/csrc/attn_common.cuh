@@ -108,13 +108,20 @@ static_assert(units_of(0x7fffffff, kManyKeys) == 1 << 24 && units_of(0x7fffffff,
 __device__ __forceinline__ int few_ctas_of(const AttnArgs &g, int64_t few) {
     return few < g.few_ctas ? static_cast<int>(few) : g.few_ctas;
 }
-// The two kernels run at the same time, on different SMs.  Where the few rows have far more to do
-// (eight times the units), the many rows take no more CTAs than have five units each, and the
-// other SMs read keys and values meanwhile.  64 sequences behind one prefix (18 times): 75 us
-// with a unit each, 69 with five, 72 with eight, 80 with twelve; 16 prompts of 8 beams (twice)
-// 29.5 with one, 30.7 with five.
+// The two kernels run at the same time, on different SMs.  Where the many rows have a unit for each
+// SM and the few rows ten for each of their CTAs, the many rows take no more CTAs than have five
+// units each, and the other SMs read keys and values meanwhile: a segment of the many rows then
+// falls to fewer CTAs, and what its beginning costs is paid less often.  us with a unit each and
+// with five, 64 sequences of 32 heads of 128 (many, few units):
+//   528, 6656  70.6  65.2     272, 8192  75.2  68.4     272, 2560  37.9  39.2
+//   528, 3584  51.4  48.7     272, 3072  41.6  41.1     80, 2560   33.2  38.2
+// Few rows with little to do do not make up for the wait for the longer runs of the many (24, 576:
+// 22.9 and 28.6; 36, 727: 22.8 and 27.7), and many rows of less than a unit an SM leave SMs free as
+// it is (18, 3120: 24.4 and 28.4; 120, 3384: 28.5 and 30.8).  (What the rule leaves: 16 sequences of
+// 14 heads of 64, one tile of rows: 68, 2048 33.6 and 31.6.)
 __device__ __forceinline__ int many_ctas_of(const AttnArgs &g, int64_t many, int64_t few) {
-    const int64_t n = few >= 8 * many ? (many + 4) / 5 : many;
+    const bool fewer = many >= g.many_ctas && few >= 10 * static_cast<int64_t>(g.few_ctas);
+    const int64_t n = fewer ? (many + 4) / 5 : many;
     return n < g.many_ctas ? static_cast<int>(n) : g.many_ctas;
 }
 __device__ __forceinline__ AttnCounts counts_at(const AttnCounts *n) {
