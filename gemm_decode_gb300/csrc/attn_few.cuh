@@ -11,12 +11,15 @@
 // One warp brings units of 64 keys into a ring of stages (bulk tensor copies, a box per page or
 // 64 rows of one, 128-byte swizzle), four warps compute: each takes 16 of a unit's keys, with a
 // running maximum, sum and accumulators of its own, joined in a fixed order when the segment
-// ends.  Two CTAs to an SM, three stages of 32 KB each (128 features).
+// ends.  Two CTAs to an SM, three stages of 32 KB each (128 features).  The weights are rounded to
+// the cache's type, as the products' other operand is of it (attn_many.cuh has what that costs).
 //
 // Measured (cold caches): own segments of 64 sequences, 768 keys on average, 8 heads of 128
 // (201 MB) 41 us, 4.9 TB/s, 0.72 of measured (38 without the fence before a stage is given back,
 // and wrong); of 256 sequences, 218 keys (228 MB) 53 us: there a segment is four units, and its
-// queries' loads and its join cost two.
+// queries' loads and its join cost two.  A batch of own segments alone, plan and join among it (graphs):
+// 64 sequences of 4000 keys (1.05 GB) 172-178 us, 5.9-6.1 TB/s, 0.87-0.90 of measured; 256 of 1076 on
+// average 188 us, 0.88; 8 of 2000 (66 MB) 19.5 us.
 #pragma once
 
 #include "attn_common.cuh"

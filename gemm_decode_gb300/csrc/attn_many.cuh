@@ -10,6 +10,10 @@
 // The maximum that a row's weights are relative to is renewed only when it has grown by more
 // than a factor of 2^8: weights up to 2^8 round as well as ones below 1, sums are binary32, and
 // the sums in tensor memory hardly ever have to be scaled.
+// Both operands of a product are of one type, so a weight is rounded once to the cache's (the sums
+// that divide are of the unrounded ones): outputs are off by 1.8-2.4e-3 (bf16) and 2.7e-4 (f16), 2-norm,
+// where their own rounding alone is 1.7e-3 and 2.1e-4.  What the rounding takes off could be a second
+// operand, for half as many MMAs again.
 //
 // One CTA per SM, twelve warps:
 //   warp 0      bulk tensor copies: queries of a segment, tiles of keys and values in turn into
@@ -27,7 +31,7 @@
 // MMAs and the weights (weights without exponentials: 3050).  A segment's beginning and end cost
 // about 2.4 units: the first scores and weights, and the results out of tensor memory.
 // Measured (graphs): 256 queries x 32 heads by 27900 keys of 8 heads 94 us, 1.25 PFLOP/s (0.65 of
-// measured bf16); a causal prompt of 4096 tokens 147 us with plan and join, 0.93 PFLOP/s.
+// measured bf16); a causal prompt of 4096 tokens 141-147 us with plan and join, 0.93-0.97 PFLOP/s.
 // Results stored 16 bytes a lane instead of whole sectors: 26 us more for the prompt.
 #pragma once
 
@@ -36,7 +40,8 @@
 namespace q4 {
 
 // The weights of a tile are handed over in two parts: those of the first keys, whose products
-// take as long as the other weights do.
+// take as long as the other weights do.  Causal prompt of 4096 and 256 sequences (graphs): 141 and
+// 160 us with 96 keys first, 145 and 163 with 64, 144 and 162 with all at once.
 constexpr int kFirstKeys = 96;
 
 template <int D>

@@ -12,10 +12,12 @@
 // the chunks of each beam, forms the scores (binary64: the order of continuations of different
 // beams whose scores are close hangs on it) and takes the K best of the group.
 //
-// Bound: latency for one group (9.7 us for four beams of 151936 tokens); for many the chain of a
-// CTA's blocks and its choice at the end: 16 groups of 8 beams of 128256 tokens (66 MB) 27 us,
-// 2.4 TB/s, 0.36 of measured.  More or fewer chunks than one wave of CTAs gains nothing (304 29.9
-// us, 608 26.9, 760 26.5, 912 34.1, 1824 41.3).
+// Bound: latency for one group (9 us for four beams of 151936 tokens: two dependent launches, each
+// a chain of loads, a sort and counts); for many the chain of a CTA's blocks and its choice at the
+// end: 16 groups of 8 beams of 128256 tokens (66 MB) 28.5 us a call on changing logits, 2.3 TB/s,
+// 0.34 of measured (21 in a graph on the same logits, which L2 holds); for wide beams the choice: 16
+// beams, K = 32, 131 us.  More or fewer chunks than one wave of CTAs gains nothing (of 152 SMs: 304
+// 29.9 us, 608 26.9, 760 26.5, 912 34.1, 1824 41.3).
 #include <algorithm>
 #include <atomic>
 

@@ -10,7 +10,7 @@
 //   join     adds the parts of each row, where several kernels or CTAs have one
 //
 // The four are launched overlapped, and the kernels for many and few rows run side by side (256
-// sequences: 162 us one after the other, 158 so).  Four beams of a prompt of 1000 tokens take
+// sequences: 162 us one after the other, 157-160 so).  Four beams of a prompt of 1000 tokens take
 // 16 us, most of it latency: the plan 3-4 us (13 us for a prompt of 4096 queries with a limit
 // each before its tables lay in shared memory and its records were those that are read), the
 // join 5.
