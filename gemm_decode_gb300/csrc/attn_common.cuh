@@ -114,7 +114,7 @@ __device__ __forceinline__ int few_ctas_of(const AttnArgs &g, int64_t few) {
 // falls to fewer CTAs, and what its beginning costs is paid less often.  us with a unit each and
 // with five, 64 sequences of 32 heads of 128 (many, few units):
 //   528, 6656  70.6  65.2     272, 8192  75.2  68.4     272, 2560  37.9  39.2
-//   528, 3584  51.4  48.7     272, 3072  41.6  41.1     80, 2560   33.2  38.2
+//   528, 3584  51.4  48.7     272, 3584  47.1  43.8     80, 2560   33.2  38.2
 // Few rows with little to do do not make up for the wait for the longer runs of the many (24, 576:
 // 22.9 and 28.6; 36, 727: 22.8 and 27.7), and many rows of less than a unit an SM leave SMs free as
 // it is (18, 3120: 24.4 and 28.4; 120, 3384: 28.5 and 30.8).  (What the rule leaves: 16 sequences of
